@@ -5,6 +5,7 @@
 
 #include <cstring>
 #include <string>
+#include <utility>
 
 #include "nsn.h"
 #include "nsn_launch.h"
@@ -180,6 +181,40 @@ nsn_status nsn_append_residual(nsn_cache* k_cache, nsn_cache* v_cache, const voi
   if (stride_b < 0 || stride_h < 0 || stride_b % e16 || stride_h % e16) return NSN_ERR_INVALID_ARG;
   return cuda_status(nsn::launch_append(view(k_cache), view(v_cache), k_new, v_new, dtype, stride_b, stride_h, cb_k,
                                         cb_v, static_cast<cudaStream_t>(stream)));
+}
+
+// Rows of 128 elements at b*sb + t*st + h*sh do not overlap: of the dimensions longer
+// than 1, each stride is past the extent of those of smaller stride.
+static bool rows_apart(int64_t nb, int64_t sb, int64_t nt, int64_t st, int64_t nh, int64_t sh) {
+  int64_t n[3] = {nb, nt, nh}, s[3] = {sb, st, sh};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (s[j] < s[i]) { std::swap(s[i], s[j]); std::swap(n[i], n[j]); }
+  int64_t extent = NSN_HEAD_DIM;
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] <= 1) continue;
+    if (s[i] < extent || s[i] > INT64_MAX / 4 / n[i]) return false;
+    extent += (n[i] - 1) * s[i];
+  }
+  return true;
+}
+
+nsn_status nsn_dequantize_kv(const nsn_cache* cache, int start, int n_tokens, const float* codebook, void* out,
+                             int dtype, int64_t stride_b, int64_t stride_t, int64_t stride_h, void* stream) {
+  const nsn_status st = check_cache(cache);
+  if (st != NSN_OK) return st;
+  if (!codebook || !aligned16(codebook) || !valid_dtype(dtype) || start < 0 || n_tokens < 0) return NSN_ERR_INVALID_ARG;
+  const int64_t e16 = elems16(dtype);
+  if (stride_b < 0 || stride_t < 0 || stride_h < 0) return NSN_ERR_INVALID_ARG;
+  if (stride_b % e16 || stride_t % e16 || stride_h % e16) return NSN_ERR_INVALID_ARG;
+  if (n_tokens == 0) return NSN_OK;
+  if (!out || !aligned16(out)) return NSN_ERR_INVALID_ARG;
+  if (!rows_apart(cache->batch, stride_b, n_tokens, stride_t, cache->n_kv_heads, stride_h)) return NSN_ERR_INVALID_ARG;
+  // no sequence has tokens past its buffers' end
+  const int64_t most = (int64_t)cache->capacity + cache->window - start;
+  if (most <= 0) return NSN_OK;
+  return cuda_status(nsn::launch_readback(view(cache), start, (int)(n_tokens < most ? n_tokens : most), codebook, out,
+                                          dtype, stride_b, stride_t, stride_h, static_cast<cudaStream_t>(stream)));
 }
 
 size_t nsn_decode_workspace_bytes(const nsn_cache* k_cache, int n_q_heads) {

@@ -52,6 +52,10 @@ cudaError_t launch_quantize_prefill(const void* x, int dtype, int64_t sb, int64_
 cudaError_t launch_append(const CacheView& kc, const CacheView& vc, const void* kn, const void* vn, int dtype,
                           int64_t sb, int64_t sh, const float* cbk, const float* cbv, cudaStream_t s);
 
+// Tokens [start, start + n_tokens) of every (b, h) as rows of `dtype` (strides in elements).
+cudaError_t launch_readback(const CacheView& cv, int start, int n_tokens, const float* cb, void* out, int dtype,
+                            int64_t sb, int64_t st, int64_t sh, cudaStream_t s);
+
 cudaError_t launch_decode(const CacheView& kc, const CacheView& vc, const void* q, int dtype, int n_q_heads,
                           int64_t qsb, int64_t qsh, float softmax_scale, const float* cbk, const float* cbv,
                           float* out, void* ws, const DecodeGeom& geom, cudaStream_t s);

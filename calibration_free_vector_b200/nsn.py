@@ -3,7 +3,7 @@ marshalling only).  Every step of the path runs in libnsn.so; there is no CPU
 fallback.  torch is used for device memory and streams only.
 
 Functions keep the C names: nsn_build_codebook_host, nsn_quantize_kv,
-nsn_append_residual, nsn_decode_workspace_bytes, nsn_decode_attention,
+nsn_append_residual, nsn_dequantize_kv, nsn_decode_workspace_bytes, nsn_decode_attention,
 nsn_decode_rope_workspace_bytes, nsn_decode_attention_rope,
 nsn_cache_buffer_sizes.  `Cache` allocates the buffers of one nsn_cache with
 torch and fills the C struct.
@@ -91,6 +91,9 @@ def load():
     lib.nsn_append_residual.restype = c_int
     lib.nsn_append_residual.argtypes = [POINTER(nsn_cache), POINTER(nsn_cache), c_void_p, c_void_p, c_int,
                                         c_int64, c_int64, c_void_p, c_void_p, c_void_p]
+    lib.nsn_dequantize_kv.restype = c_int
+    lib.nsn_dequantize_kv.argtypes = [POINTER(nsn_cache), c_int, c_int, c_void_p, c_void_p, c_int, c_int64, c_int64,
+                                      c_int64, c_void_p]
     lib.nsn_decode_workspace_bytes.restype = c_size_t
     lib.nsn_decode_workspace_bytes.argtypes = [POINTER(nsn_cache), c_int]
     lib.nsn_decode_attention.restype = c_int
@@ -276,6 +279,41 @@ def nsn_append_residual(k_cache: Cache, v_cache: Cache, k_new, v_new, cb_k, cb_v
                                     v_new.data_ptr(), _dtype_code(k_new), k_new.stride(0), k_new.stride(1),
                                     cb_k.data_ptr(), cb_v.data_ptr(), _stream_ptr(stream))
     _check(st, "nsn_append_residual")
+
+
+def _one_device(first, *others):
+    """The device of `first`, which the other tensors must share; the call is made with it current."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    return first.device
+
+
+def _check_codebook(*codebooks) -> None:
+    import torch
+    for cb in codebooks:
+        if cb.dtype != torch.float32 or cb.numel() != N_CODES * SUB_DIM or not cb.is_contiguous():
+            raise ValueError("a codebook must be a contiguous float32 tensor of 256 x 8")
+
+
+def nsn_dequantize_kv(cache: Cache, out, codebook, start: int = 0, stream=None) -> None:
+    """Reads tokens start .. start + T - 1 of every (b, h) back into out [B, T, H_kv, 128]
+    (float32, bfloat16 or float16; any non-overlapping strides with unit last dim): the
+    quantized tokens reconstructed, the window tokens as they are.  Rows of tokens that a
+    sequence does not have are left as they were."""
+    if out.dim() != 4 or out.shape[-1] != HEAD_DIM or out.stride(-1) != 1:
+        raise ValueError("out must be [B, T, H_kv, 128] with a contiguous last dimension")
+    if out.shape[0] != cache.batch or out.shape[2] != cache.n_kv_heads:
+        raise ValueError("out batch / kv-head count does not match the cache")
+    if start < 0:
+        raise ValueError("start must not be negative")
+    _check_codebook(codebook)
+    import torch
+    with torch.cuda.device(_one_device(cache.codes, out, codebook)):
+        st = load().nsn_dequantize_kv(ctypes.byref(cache.c), start, out.shape[1], codebook.data_ptr(), out.data_ptr(),
+                                      _dtype_code(out), out.stride(0), out.stride(1), out.stride(2),
+                                      _stream_ptr(stream))
+    _check(st, "nsn_dequantize_kv")
 
 
 def nsn_selftest_bounded_wait(status, max_attempts: int = 8, stream=None) -> None:

@@ -255,6 +255,27 @@ nsn_status nsn_append_residual(nsn_cache* k_cache, nsn_cache* v_cache, const voi
                                const float* cb_k, const float* cb_v, void* stream);
 
 /*
+ * Reads a cache back: tokens start .. start + n_tokens - 1 of every (b, h) as ordinary
+ * rows ([TS] Metodologia 3 and 4: dequantization, the inverse of the steps above; the
+ * fp16 residual window follows the quantized tokens).
+ *   row (b, t, h) at out + b*stride_b + (t-start)*stride_t + h*stride_h  :=
+ *     H^T ((u_hat s2 + o) s1)        t < n_quant      (in fp32, rounded once to dtype)
+ *     window[t - n_quant]            n_quant <= t < n_quant + n_window
+ * Rows of tokens that the (b, h) does not have are left as they were.
+ *   codebook   device float[256*8], read rounded to fp16 (as the decode reads it).
+ *   out        device, dtype element type, 16-byte aligned rows of 128 values that do
+ *              not overlap (every stride of a dimension longer than 1 at least 128, and
+ *              past the extent of the dimensions of smaller stride).
+ *   start      >= 0; n_tokens >= 0 (0: nothing is launched; out may be NULL).
+ * For double_quant caches s1 and o are the values of their 4-bit levels.  Keys come back
+ * as they were given to the quantizer (pre-RoPE keys without RoPE).  The cache is not
+ * changed.  One launch.
+ */
+nsn_status nsn_dequantize_kv(const nsn_cache* cache, int start, int n_tokens, const float* codebook,
+                             void* out, int dtype, int64_t stride_b, int64_t stride_t,
+                             int64_t stride_h, void* stream);
+
+/*
  * Workspace bytes that nsn_decode_attention needs for these caches and n_q_heads.
  * The workspace starts with 2 * batch * n_kv_heads 32-bit merge counters (padded
  * to 256 bytes); the decode partials follow.
