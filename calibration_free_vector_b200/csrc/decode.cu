@@ -434,11 +434,13 @@ __device__ __forceinline__ void store_partial(SoftmaxState& st, float* __restric
 // hold the quantized part (rotated domain), slot nsplit the residual window
 // (original domain).  The rotated value sum is taken back with H (H^T = H)
 // before both parts are normalised together.  Partials written by other SMs are
-// read through L2.  `scratch` is shared memory no longer in use (the stage
+// read through L2.  `lse_rows` (may be null) receives each row's (max in log2 units,
+// denominator), for a caller that joins the rows with another part of the sequence.
+// `scratch` is shared memory no longer in use (the stage
 // buffers): (nsplit + 1) * GH float2 weights, then GH * 128 floats.
 template <int GH>
 __device__ __noinline__ void cta_merge(const float* ws, const float* ws_acc, int64_t p0, int nsplit, int G, int hbase,
-                                       float* __restrict__ out_rows, float* scratch) {
+                                       float* __restrict__ out_rows, float2* __restrict__ lse_rows, float* scratch) {
   constexpr int CH = 32;  // slots whose accumulators a thread holds in registers at once
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nslot = nsplit + 1;
@@ -513,6 +515,7 @@ __device__ __noinline__ void cta_merge(const float* ws, const float* ws_acc, int
     o.z = (a[2] * INV_SQRT_D * fa + aw[2] * fr) * inv;
     o.w = (a[3] * INV_SQRT_D * fa + aw[3] * fr) * inv;
     *reinterpret_cast<float4*>(out_rows + (int64_t)hh * D + 4 * lane) = o;
+    if (lse_rows && lane == 0) lse_rows[hh] = make_float2(mt, den);
   }
   __syncthreads();  // the scratch may be reused by the next merge of this CTA
 }
@@ -539,7 +542,8 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, 1)
 decode_kernel(CacheView kc, CacheView vc, const void* __restrict__ q, int dtype, int64_t qsb, int64_t qsh,
               float qscale, const float* __restrict__ cbk_g, const float* __restrict__ cbv_g,
               unsigned int* __restrict__ counters, float* __restrict__ ws, float* __restrict__ out, int n_q_heads,
-              DecodeGeom geom, const float* __restrict__ rscores, int rs_cap, int nw_cut, int64_t out_sb) {
+              DecodeGeom geom, const float* __restrict__ rscores, int rs_cap, int nw_cut, int64_t out_sb,
+              float2* __restrict__ lse) {
   static_assert(GH == 1 || GH == 2 || GH == 4, "1, 2 or 4 heads per warp");
   extern __shared__ __align__(128) unsigned char smem_raw[];
   DecSmem& sm = *reinterpret_cast<DecSmem*>(smem_raw);
@@ -946,7 +950,8 @@ decode_kernel(CacheView kc, CacheView vc, const void* __restrict__ q, int dtype,
     const int mseq = sm.merge_seq[m], mhg = sm.merge_hg[m];
     const int mb = mseq / kc.n_kv_heads, mhk = mseq % kc.n_kv_heads;
     cta_merge<GH>(ws, ws + acc_offset(P, G), (int64_t)mseq * (nsplit + 1), nsplit, G, mhg * GH,
-                  out + (int64_t)mb * out_sb + (int64_t)(mhk * G + mhg * GH) * D, scratch);
+                  out + (int64_t)mb * out_sb + (int64_t)(mhk * G + mhg * GH) * D,
+                  lse ? lse + (int64_t)mb * n_q_heads + mhk * G + mhg * GH : nullptr, scratch);
   }
 }
 
@@ -1331,6 +1336,8 @@ DecodeGeom decode_geometry(int batch, int capacity, int n_q_heads, int n_kv_head
 // padded to 256 bytes.
 static int64_t counter_words(int64_t nseq) { return ((2 * nseq + 63) / 64) * 64; }
 
+size_t decode_counter_bytes(int batch, int n_kv_heads) { return (size_t)counter_words((int64_t)batch * n_kv_heads) * 4u; }
+
 size_t decode_partial_bytes(int batch, int n_kv_heads, const DecodeGeom& geom) {
   const int64_t P = (int64_t)batch * n_kv_heads * (geom.nsplit_q + 1);
   return (size_t)(acc_offset(P, geom.g) + P * geom.g * D) * sizeof(float);
@@ -1344,7 +1351,7 @@ template <int G, int MK, int MV, bool DQ>
 static cudaError_t launch_t(const CacheView& kc, const CacheView& vc, const void* q, int dtype, int n_q_heads,
                             int64_t qsb, int64_t qsh, float qscale, const float* cbk, const float* cbv, float* out,
                             unsigned int* counters, float* partials, const DecodeGeom& geom, cudaStream_t s,
-                            int nw_cut, int64_t out_sb) {
+                            int nw_cut, int64_t out_sb, float2* lse) {
   constexpr int GH = G < 4 ? G : 4;  // heads per warp job
   const size_t smem = sizeof(DecSmem);
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<GH, MK, MV, DQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1354,7 +1361,7 @@ static cudaError_t launch_t(const CacheView& kc, const CacheView& vc, const void
   dim3 grid((nwarps + DEC_WARPS - 1) / DEC_WARPS);
   decode_kernel<GH, MK, MV, DQ><<<grid, 32 * DEC_WARPS, smem, s>>>(kc, vc, q, dtype, qsb, qsh, qscale, cbk, cbv,
                                                                counters, partials, out, n_q_heads, geom, nullptr, 0,
-                                                               nw_cut, out_sb);
+                                                               nw_cut, out_sb, lse);
   return cudaGetLastError();
 }
 
@@ -1362,12 +1369,12 @@ template <int G>
 static cudaError_t launch_g(const CacheView& kc, const CacheView& vc, const void* q, int dtype, int n_q_heads,
                             int64_t qsb, int64_t qsh, float qscale, const float* cbk, const float* cbv, float* out,
                             unsigned int* counters, float* partials, const DecodeGeom& geom, cudaStream_t s,
-                            int nw_cut, int64_t out_sb) {
+                            int nw_cut, int64_t out_sb, float2* lse) {
 #define NSN_LAUNCH(MK_, MV_)                                                                                    \
   return kc.dq ? launch_t<G, MK_, MV_, true>(kc, vc, q, dtype, n_q_heads, qsb, qsh, qscale, cbk, cbv, out, counters,  \
-                                             partials, geom, s, nw_cut, out_sb)                                       \
+                                             partials, geom, s, nw_cut, out_sb, lse)                                  \
                : launch_t<G, MK_, MV_, false>(kc, vc, q, dtype, n_q_heads, qsb, qsh, qscale, cbk, cbv, out, counters, \
-                                              partials, geom, s, nw_cut, out_sb)
+                                              partials, geom, s, nw_cut, out_sb, lse)
   if (kc.mode == NSN_MODE_1BIT && vc.mode == NSN_MODE_1BIT) NSN_LAUNCH(1, 1);
   if (kc.mode == NSN_MODE_1BIT && vc.mode == NSN_MODE_2BIT) NSN_LAUNCH(1, 2);
   if (kc.mode == NSN_MODE_2BIT && vc.mode == NSN_MODE_1BIT) NSN_LAUNCH(2, 1);
@@ -1378,12 +1385,12 @@ static cudaError_t launch_g(const CacheView& kc, const CacheView& vc, const void
 static cudaError_t launch_any(const CacheView& kc, const CacheView& vc, const void* q, int dtype, int n_q_heads,
                               int64_t qsb, int64_t qsh, float softmax_scale, const float* cbk, const float* cbv,
                               float* out, unsigned int* counters, float* partials, const DecodeGeom& geom,
-                              cudaStream_t s, int nw_cut = 0, int64_t out_sb = -1) {
+                              cudaStream_t s, int nw_cut = 0, int64_t out_sb = -1, float2* lse = nullptr) {
   const float qscale = softmax_scale * LOG2E;
   if (out_sb < 0) out_sb = (int64_t)n_q_heads * D;
 #define NSN_G(G_) \
   return launch_g<G_>(kc, vc, q, dtype, n_q_heads, qsb, qsh, qscale, cbk, cbv, out, counters, partials, geom, s, \
-                      nw_cut, out_sb)
+                      nw_cut, out_sb, lse)
   switch (geom.g) {
     case 1: NSN_G(1);
     case 2: NSN_G(2);
@@ -1399,6 +1406,15 @@ cudaError_t launch_decode(const CacheView& kc, const CacheView& vc, const void* 
   unsigned int* counters = static_cast<unsigned int*>(ws);
   float* partials = static_cast<float*>(ws) + counter_words((int64_t)kc.batch * kc.n_kv_heads);
   return launch_any(kc, vc, q, dtype, n_q_heads, qsb, qsh, softmax_scale, cbk, cbv, out, counters, partials, geom, s);
+}
+
+cudaError_t launch_decode_lse(const CacheView& kc, const CacheView& vc, const void* q, int dtype, int n_q_heads,
+                              int64_t qsb, int64_t qsh, float softmax_scale, const float* cbk, const float* cbv,
+                              float* out, float2* lse, void* ws, const DecodeGeom& geom, cudaStream_t s) {
+  unsigned int* counters = static_cast<unsigned int*>(ws);
+  float* partials = static_cast<float*>(ws) + counter_words((int64_t)kc.batch * kc.n_kv_heads);
+  return launch_any(kc, vc, q, dtype, n_q_heads, qsb, qsh, softmax_scale, cbk, cbv, out, counters, partials, geom, s, 0,
+                    -1, lse);
 }
 
 // Chunked-prefill ("extend") attention: the last n_queries tokens of every
@@ -1471,7 +1487,7 @@ static cudaError_t launch_rope_t(const CacheView& kc, const CacheView& vc, const
   const int nwarps = nseq * geom.nsplit_q * (G / GH);
   decode_kernel<GH, NSN_MODE_2BIT, MV, DQ, true><<<(nwarps + DEC_WARPS - 1) / DEC_WARPS, 32 * DEC_WARPS, smem, s>>>(
       kc, vc, q, dtype, qsb, qsh, qscale, cbk, cbv, counters, partials, out, n_q_heads, geom, rscores, rs_cap, 0,
-      (int64_t)n_q_heads * D);
+      (int64_t)n_q_heads * D, nullptr);
   return cudaGetLastError();
 }
 

@@ -277,6 +277,75 @@ nsn_status nsn_extend_attention(const nsn_cache* k_cache, const nsn_cache* v_cac
                                         static_cast<cudaStream_t>(stream)));
 }
 
+// The caches and sizes of a shared-prefix call.
+static nsn_status check_prefix(const nsn_cache* prefix_k, const nsn_cache* k_cache, int n_q_heads, int n_queries) {
+  nsn_status st = check_cache(prefix_k);
+  if (st != NSN_OK) return st;
+  st = check_cache(k_cache);
+  if (st != NSN_OK) return st;
+  if (prefix_k->batch != 1 || prefix_k->n_kv_heads != k_cache->n_kv_heads || prefix_k->mode != k_cache->mode ||
+      prefix_k->double_quant != k_cache->double_quant)
+    return NSN_ERR_INVALID_ARG;
+  if (n_q_heads <= 0 || n_q_heads % k_cache->n_kv_heads) return NSN_ERR_INVALID_ARG;
+  if (n_queries < 1 || n_queries > NSN_BLOCK) return NSN_ERR_INVALID_ARG;
+  const int g = n_q_heads / k_cache->n_kv_heads;
+  if (g != 1 && g != 2 && g != 4 && g != 8) return NSN_ERR_UNSUPPORTED;
+  // row, item and block counts stay well inside 32 bits
+  if ((int64_t)k_cache->batch * n_queries * n_q_heads > (1 << 28)) return NSN_ERR_UNSUPPORTED;
+  return NSN_OK;
+}
+
+size_t nsn_prefix_workspace_bytes(const nsn_cache* prefix_k, const nsn_cache* k_cache, int n_q_heads, int n_queries) {
+  if (check_prefix(prefix_k, k_cache, n_q_heads, n_queries) != NSN_OK) return 0;
+  return nsn::prefix_workspace_bytes(k_cache->batch, k_cache->n_kv_heads, n_q_heads / k_cache->n_kv_heads, n_queries,
+                                     k_cache->capacity);
+}
+
+static nsn_status attention_prefix(const nsn_cache* prefix_k, const nsn_cache* prefix_v, const nsn_cache* k_cache,
+                                   const nsn_cache* v_cache, const void* q, int dtype, int n_q_heads, int n_queries,
+                                   bool causal, int64_t q_stride_b, int64_t q_stride_t, int64_t q_stride_h,
+                                   float softmax_scale, const float* cb_k, const float* cb_v, void* out, int out_dtype,
+                                   void* workspace, size_t ws_bytes, void* stream) {
+  nsn_status st = check_prefix(prefix_k, k_cache, n_q_heads, n_queries);
+  if (st != NSN_OK) return st;
+  st = check_prefix(prefix_v, v_cache, n_q_heads, n_queries);
+  if (st != NSN_OK) return st;
+  if (!same_shape(prefix_k, prefix_v) || !same_shape(k_cache, v_cache)) return NSN_ERR_INVALID_ARG;
+  if (causal && k_cache->window == 0) return NSN_ERR_UNSUPPORTED;
+  if (!q || !cb_k || !cb_v || !out || !workspace || !valid_dtype(dtype) || !valid_dtype(out_dtype))
+    return NSN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(cb_k) || !aligned16(cb_v) || !aligned16(out)) return NSN_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return NSN_ERR_INVALID_ARG;
+  const int64_t e16 = elems16(dtype);
+  if (q_stride_b < 0 || q_stride_t < 0 || q_stride_h < 0 || q_stride_b % e16 || q_stride_t % e16 || q_stride_h % e16)
+    return NSN_ERR_INVALID_ARG;
+  if (!(softmax_scale == softmax_scale)) return NSN_ERR_INVALID_ARG;
+  if (ws_bytes < nsn::prefix_workspace_bytes(k_cache->batch, k_cache->n_kv_heads, n_q_heads / k_cache->n_kv_heads, n_queries,
+                                            k_cache->capacity))
+    return NSN_ERR_WORKSPACE;
+  return cuda_status(nsn::launch_prefix(view(prefix_k), view(prefix_v), view(k_cache), view(v_cache), q, dtype, n_q_heads,
+                                        n_queries, causal, q_stride_b, q_stride_t, q_stride_h, softmax_scale, cb_k, cb_v,
+                                        out, out_dtype, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+nsn_status nsn_decode_attention_prefix(const nsn_cache* prefix_k, const nsn_cache* prefix_v, const nsn_cache* k_cache,
+                                       const nsn_cache* v_cache, const void* q, int dtype, int n_q_heads,
+                                       int64_t q_stride_b, int64_t q_stride_h, float softmax_scale, const float* cb_k,
+                                       const float* cb_v, void* out, int out_dtype, void* workspace, size_t ws_bytes,
+                                       void* stream) {
+  return attention_prefix(prefix_k, prefix_v, k_cache, v_cache, q, dtype, n_q_heads, 1, false, q_stride_b, 0, q_stride_h,
+                          softmax_scale, cb_k, cb_v, out, out_dtype, workspace, ws_bytes, stream);
+}
+
+nsn_status nsn_extend_attention_prefix(const nsn_cache* prefix_k, const nsn_cache* prefix_v, const nsn_cache* k_cache,
+                                       const nsn_cache* v_cache, const void* q, int dtype, int n_q_heads, int n_queries,
+                                       int64_t q_stride_b, int64_t q_stride_t, int64_t q_stride_h, float softmax_scale,
+                                       const float* cb_k, const float* cb_v, void* out, int out_dtype, void* workspace,
+                                       size_t ws_bytes, void* stream) {
+  return attention_prefix(prefix_k, prefix_v, k_cache, v_cache, q, dtype, n_q_heads, n_queries, true, q_stride_b,
+                          q_stride_t, q_stride_h, softmax_scale, cb_k, cb_v, out, out_dtype, workspace, ws_bytes, stream);
+}
+
 size_t nsn_decode_rope_workspace_bytes(const nsn_cache* k_cache, int n_q_heads) {
   if (check_cache(k_cache) != NSN_OK || n_q_heads <= 0 || n_q_heads % k_cache->n_kv_heads) return 0;
   const nsn::DecodeGeom g = nsn::decode_geometry(k_cache->batch, k_cache->capacity, n_q_heads, k_cache->n_kv_heads);

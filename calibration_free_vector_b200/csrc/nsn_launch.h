@@ -37,6 +37,7 @@ struct DecodeGeom {
 DecodeGeom decode_geometry(int batch, int capacity, int n_q_heads, int n_kv_heads);
 // Workspace = merge counters (zero at rest) followed by the partials.
 size_t decode_workspace_bytes(int batch, int n_kv_heads, const DecodeGeom& geom);
+size_t decode_counter_bytes(int batch, int n_kv_heads);
 size_t decode_partial_bytes(int batch, int n_kv_heads, const DecodeGeom& geom);
 // Whether a shape fits the allocation-free decode's fixed arrays.
 bool decode_static_fits(int batch, int n_kv_heads, const DecodeGeom& geom);
@@ -60,10 +61,24 @@ cudaError_t launch_decode(const CacheView& kc, const CacheView& vc, const void* 
                           int64_t qsb, int64_t qsh, float softmax_scale, const float* cbk, const float* cbv,
                           float* out, void* ws, const DecodeGeom& geom, cudaStream_t s);
 
+// launch_decode that also writes each row's (max in log2 units, denominator) to lse[b][q-head].
+cudaError_t launch_decode_lse(const CacheView& kc, const CacheView& vc, const void* q, int dtype, int n_q_heads,
+                              int64_t qsb, int64_t qsh, float softmax_scale, const float* cbk, const float* cbv,
+                              float* out, float2* lse, void* ws, const DecodeGeom& geom, cudaStream_t s);
+
 // Chunked-prefill attention of the last n_queries window tokens (causal inside the window).
 cudaError_t launch_extend(const CacheView& kc, const CacheView& vc, const void* q, int dtype, int n_q_heads,
                           int n_queries, int64_t qsb, int64_t qst, int64_t qsh, float softmax_scale, const float* cbk,
                           const float* cbv, float* out, void* ws, const DecodeGeom& geom, cudaStream_t s);
+
+// Attention over a prefix that the whole batch shares (caches of batch 1) and each
+// sequence's own cache.  `causal`: the last n_queries tokens of every sequence sit in its
+// window and query c sees the window up to its own token.
+size_t prefix_workspace_bytes(int batch, int n_kv_heads, int g, int n_queries, int own_capacity);
+cudaError_t launch_prefix(const CacheView& pk, const CacheView& pv, const CacheView& k, const CacheView& v, const void* q,
+                          int dtype, int n_q_heads, int n_queries, bool causal, int64_t qsb, int64_t qst, int64_t qsh,
+                          float softmax_scale, const float* cbk, const float* cbv, void* out, int out_dtype, void* ws,
+                          cudaStream_t s);
 
 // Pre-RoPE keys: the K logits (keys rotated at their positions by inv_freq) into
 // the workspace after the decode partials, then the decode over them.

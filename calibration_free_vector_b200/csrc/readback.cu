@@ -6,18 +6,12 @@
 // so H is applied to the codewords themselves, which are exact in fp16, and the norms
 // enter in fp32 afterwards; H o_b is formed once per unit of work.
 //
-// H of 128 values is the Kronecker product H8 (x) H16.  Dim d = 16 r + c:
-//   - the H16 factor runs on the tensor cores: for each r, the 16 tokens of a tile times
-//     the 16 values of sub-vectors 2r and 2r + 1 (M = tokens, K = 16), against the 16 x 16
-//     matrix of +-1.  The A operand is gathered by ldmatrix straight from an 8-fold
-//     replicated fp16 codebook, the stored signs XOR-ed on.  Sums of 16 codeword entries
-//     in fp32.
-//   - the H8 factor is three butterfly stages over r: a thread holds all eight r of its
-//     (token, column)s, so they are register additions.
-// The columns of H16 are dealt to the two n-tiles so that a thread ends with four
-// consecutive dims of a row: 8- or 16-byte stores, every 32-byte sector written whole.
+// The transform is the one of hadamard_mma.cuh (M = the 16 tokens of a tile).  Its A operand,
+// for each r the 16 values of sub-vectors 2r and 2r + 1, is gathered by ldmatrix straight from an
+// 8-fold replicated fp16 codebook, the stored signs XOR-ed on.  A lane ends with four consecutive
+// dims of a row: 8- or 16-byte stores, every 32-byte sector written whole.
 
-#include "nsn_common.cuh"
+#include "hadamard_mma.cuh"
 #include "nsn_launch.h"
 
 namespace nsn {
@@ -37,31 +31,6 @@ __device__ __forceinline__ void rb_ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
-}
-
-// d += A (16 tokens x 16) * B (16 x 8), fp16 operands, fp32 sums.
-__device__ __forceinline__ void rb_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// The H8 factor: butterflies over r of the accumulators [r][n-tile][4].
-__device__ __forceinline__ void rb_butterflies(float (&E)[8][2][4]) {
-#pragma unroll
-  for (int step = 1; step < 8; step <<= 1)
-#pragma unroll
-    for (int a = 0; a < 8; ++a)
-      if (!(a & step))
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float u = E[a][nt][i], w = E[a + step][nt][i];
-            E[a][nt][i] = u + w;
-            E[a + step][nt][i] = u - w;
-          }
 }
 
 __device__ __forceinline__ uint32_t rb_pack(float x, float y, int dt) {
@@ -137,18 +106,8 @@ readback_kernel(CacheView cv, int start, int n_tokens, const float* __restrict__
   __syncthreads();
   const uint32_t cb_base = (uint32_t)__cvta_generic_to_shared(&sm.cb[0][0]) + (uint32_t)(lane & 7) * 16u;
 
-  // B fragments of H16: rows k = 2p, 2p+1 (+8), column c of n-tile column g
   uint32_t hb[2][2];
-#pragma unroll
-  for (int nt = 0; nt < 2; ++nt) {
-    const int c = 4 * (g >> 1) + 2 * nt + (g & 1);
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const int k = 2 * p + 8 * kk;
-      const uint32_t lo = (__popc(k & c) & 1) ? 0xBC00u : 0x3C00u, hi = (__popc((k + 1) & c) & 1) ? 0xBC00u : 0x3C00u;
-      hb[nt][kk] = lo | (hi << 16);
-    }
-  }
+  h16_operand(hb, lane);
 
   const int unit_tok = 16 * unit_tiles;
   const int first_unit = start / unit_tok;
@@ -196,11 +155,11 @@ readback_kernel(CacheView cv, int start, int n_tokens, const float* __restrict__
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
             E[r][nt][0] = E[r][nt][1] = E[r][nt][2] = E[r][nt][3] = 0.f;
-            rb_mma(E[r][nt], ah, hb[nt][0], hb[nt][1]);
-            if constexpr (DQ) rb_mma(E[r][nt], al, hb[nt][0], hb[nt][1]);
+            h16_mma(E[r][nt], ah, hb[nt]);
+            if constexpr (DQ) h16_mma(E[r][nt], al, hb[nt]);
           }
         }
-        rb_butterflies(E);
+        h8_butterflies(E);
         __syncwarp();  // the previous unit's rows are written
         if (g == 0) {
 #pragma unroll
@@ -227,10 +186,10 @@ readback_kernel(CacheView cv, int start, int n_tokens, const float* __restrict__
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
             E[r][nt][0] = E[r][nt][1] = E[r][nt][2] = E[r][nt][3] = 0.f;
-            rb_mma(E[r][nt], a, hb[nt][0], hb[nt][1]);
+            h16_mma(E[r][nt], a, hb[nt]);
           }
         }
-        rb_butterflies(E);
+        h8_butterflies(E);
         const int t = t0 + g;
         const bool have[2] = {t >= lo && t < qhi, t + 8 >= lo && t + 8 < qhi};
         const int64_t off = row0 + (int64_t)t * st + 4 * p;

@@ -5,6 +5,7 @@ fallback.  torch is used for device memory and streams only.
 Functions keep the C names: nsn_build_codebook_host, nsn_quantize_kv,
 nsn_append_residual, nsn_dequantize_kv, nsn_decode_workspace_bytes, nsn_decode_attention,
 nsn_decode_rope_workspace_bytes, nsn_decode_attention_rope,
+nsn_prefix_workspace_bytes, nsn_decode_attention_prefix, nsn_extend_attention_prefix,
 nsn_cache_buffer_sizes.  `Cache` allocates the buffers of one nsn_cache with
 torch and fills the C struct.
 """
@@ -104,6 +105,15 @@ def load():
     lib.nsn_extend_attention.argtypes = [POINTER(nsn_cache), POINTER(nsn_cache), c_void_p, c_int, c_int, c_int,
                                          c_int64, c_int64, c_int64, c_float, c_void_p, c_void_p, c_void_p, c_void_p,
                                          c_size_t, c_void_p]
+    lib.nsn_prefix_workspace_bytes.restype = c_size_t
+    lib.nsn_prefix_workspace_bytes.argtypes = [POINTER(nsn_cache), POINTER(nsn_cache), c_int, c_int]
+    caches = [POINTER(nsn_cache)] * 4
+    lib.nsn_decode_attention_prefix.restype = c_int
+    lib.nsn_decode_attention_prefix.argtypes = caches + [c_void_p, c_int, c_int, c_int64, c_int64, c_float, c_void_p,
+                                                         c_void_p, c_void_p, c_int, c_void_p, c_size_t, c_void_p]
+    lib.nsn_extend_attention_prefix.restype = c_int
+    lib.nsn_extend_attention_prefix.argtypes = caches + [c_void_p, c_int, c_int, c_int, c_int64, c_int64, c_int64, c_float,
+                                                         c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_size_t, c_void_p]
     lib.nsn_decode_rope_workspace_bytes.restype = c_size_t
     lib.nsn_decode_rope_workspace_bytes.argtypes = [POINTER(nsn_cache), c_int]
     lib.nsn_decode_attention_rope.restype = c_int
@@ -375,6 +385,67 @@ def nsn_extend_attention(k_cache: Cache, v_cache: Cache, q, softmax_scale: float
                                      float(softmax_scale), cb_k.data_ptr(), cb_v.data_ptr(), out.data_ptr(),
                                      workspace.data_ptr(), workspace.numel(), _stream_ptr(stream))
     _check(st, "nsn_extend_attention")
+
+
+def nsn_prefix_workspace_bytes(prefix_k: Cache, k_cache: Cache, n_q_heads: int, n_queries: int = 1) -> int:
+    return int(load().nsn_prefix_workspace_bytes(ctypes.byref(prefix_k.c), ctypes.byref(k_cache.c), n_q_heads,
+                                                 n_queries))
+
+
+def prefix_workspace(prefix_k: Cache, k_cache: Cache, n_q_heads: int, n_queries: int = 1):
+    """Workspace of the shared-prefix calls with n_queries queries per sequence (zero-filled: with one
+    query it starts with merge counters, as decode_workspace)."""
+    import torch
+    n = nsn_prefix_workspace_bytes(prefix_k, k_cache, n_q_heads, n_queries)
+    if n == 0:
+        raise ValueError("invalid caches, head count or query count for a shared prefix")
+    return torch.zeros((n,), dtype=torch.uint8, device=k_cache.codes.device)
+
+
+def _check_prefix_call(prefix_k, prefix_v, k_cache, v_cache, q, cb_k, cb_v, out, workspace):
+    if q.shape[-1] != HEAD_DIM or q.stride(-1) != 1 or q.shape[0] != k_cache.batch:
+        raise ValueError("q must be [B, ..., H_q, 128] with the batch of the caches and a contiguous last dimension")
+    if not out.is_contiguous() or tuple(out.shape) != tuple(q.shape):
+        raise ValueError("out must be a contiguous tensor shaped like q")
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    _check_codebook(cb_k, cb_v)
+    return _one_device(q, prefix_k.codes, prefix_v.codes, k_cache.codes, v_cache.codes, cb_k, cb_v, out, workspace)
+
+
+def nsn_decode_attention_prefix(prefix_k: Cache, prefix_v: Cache, k_cache: Cache, v_cache: Cache, q,
+                                softmax_scale: float, cb_k, cb_v, out, workspace, stream=None) -> None:
+    """Decode attention q [B, H_q, 128] -> out [B, H_q, 128] (float32, bfloat16 or float16) over a
+    prefix that the batch shares (caches of batch 1) and each sequence's own caches."""
+    if q.dim() != 3:
+        raise ValueError("q must be [B, H_q, 128]")
+    import torch
+    device = _check_prefix_call(prefix_k, prefix_v, k_cache, v_cache, q, cb_k, cb_v, out, workspace)
+    with torch.cuda.device(device):
+        st = load().nsn_decode_attention_prefix(
+            ctypes.byref(prefix_k.c), ctypes.byref(prefix_v.c), ctypes.byref(k_cache.c), ctypes.byref(v_cache.c),
+            q.data_ptr(), _dtype_code(q), q.shape[1], q.stride(0), q.stride(1), float(softmax_scale), cb_k.data_ptr(),
+            cb_v.data_ptr(), out.data_ptr(), _dtype_code(out), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    _check(st, "nsn_decode_attention_prefix")
+
+
+def nsn_extend_attention_prefix(prefix_k: Cache, prefix_v: Cache, k_cache: Cache, v_cache: Cache, q,
+                                softmax_scale: float, cb_k, cb_v, out, workspace, stream=None) -> None:
+    """Chunked-prefill attention behind a shared prefix: q [B, C, H_q, 128] (the last C tokens of
+    every own cache, all in its window) -> out [B, C, H_q, 128]; query i attends the prefix, the own
+    quantized tokens and the own window up to its own token."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, C, H_q, 128]")
+    import torch
+    device = _check_prefix_call(prefix_k, prefix_v, k_cache, v_cache, q, cb_k, cb_v, out, workspace)
+    with torch.cuda.device(device):
+        st = load().nsn_extend_attention_prefix(
+            ctypes.byref(prefix_k.c), ctypes.byref(prefix_v.c), ctypes.byref(k_cache.c), ctypes.byref(v_cache.c),
+            q.data_ptr(), _dtype_code(q), q.shape[2], q.shape[1], q.stride(0), q.stride(1), q.stride(2),
+            float(softmax_scale), cb_k.data_ptr(), cb_v.data_ptr(), out.data_ptr(), _dtype_code(out),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    _check(st, "nsn_extend_attention_prefix")
 
 
 def nsn_decode_rope_workspace_bytes(k_cache: Cache, n_q_heads: int) -> int:

@@ -340,6 +340,63 @@ nsn_status nsn_extend_attention(const nsn_cache* k_cache, const nsn_cache* v_cac
                                 float* out, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * Decode attention of a batch that shares a prefix (one prompt, many samples or users):
+ * the prefix is compressed once, into caches of batch 1, and every sequence's own tokens
+ * into its own caches ([TS] Metodologia 4, for the sequence prefix + own tokens).  For
+ * every (b, q-head), with one softmax over both parts,
+ *   out[b][j] = attention of q[b][j] over { prefix tokens, quantized and window } U
+ *               { own quantized tokens of b } U { own window tokens of b }
+ * The prefix is read once for the whole batch, on the tensor cores.
+ *   prefix_k, prefix_v  batch 1, window 0 or 128; the n_kv_heads, modes and double_quant
+ *                  of the own caches (they share codebooks).  Counters as everywhere.
+ *   k_cache, v_cache  own caches, window 0 or 128.  A (b, h) may hold no token; where the
+ *                  prefix is empty too, its output rows are zeros.
+ *   q, n_q_heads, softmax_scale, cb_k, cb_v   as nsn_decode_attention.  |softmax_scale *
+ *                  log2(e) * H q| has to stay below 65504 (fp16).
+ *   out            device, out_dtype, [batch][n_q_heads][128].
+ *   workspace      >= nsn_prefix_workspace_bytes(..., n_queries = 1), 256-byte aligned,
+ *                  zero-filled before its first use with caches of a given batch x n_kv_heads
+ *                  (it starts with the workspace of nsn_decode_attention for the own caches, and
+ *                  its counters are left at zero in the same way).  Calls sharing one workspace
+ *                  must not overlap on the GPU.
+ * Queries, reconstructed rows and softmax weights are rounded to fp16 for the tensor
+ * cores (rows relative to the largest norm of their 128-token block); sums are fp32.  An
+ * output is off by about 5e-4 of its size, whatever out_dtype is.
+ * Three kernel launches: the own caches (the kernel of nsn_decode_attention), the prefix, the join.  Status bit 2 of k_cache->status is set if a wait inside the kernel
+ * ran out (the outputs are then not meaningful).
+ */
+size_t nsn_prefix_workspace_bytes(const nsn_cache* prefix_k, const nsn_cache* k_cache, int n_q_heads,
+                                  int n_queries);
+nsn_status nsn_decode_attention_prefix(const nsn_cache* prefix_k, const nsn_cache* prefix_v,
+                                       const nsn_cache* k_cache, const nsn_cache* v_cache, const void* q,
+                                       int dtype, int n_q_heads, int64_t q_stride_b, int64_t q_stride_h,
+                                       float softmax_scale, const float* cb_k, const float* cb_v, void* out,
+                                       int out_dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Chunked-prefill attention behind a shared prefix: nsn_extend_attention over the prefix
+ * and the own caches.  After a chunk of n_queries tokens has been added to every own cache
+ * (they are its last tokens and all sit in its window), query i of the chunk attends
+ *   { prefix tokens } U { own quantized tokens } U { own window slots 0 .. n_window - n_queries + i }
+ * with one softmax.  What a later token of the chunk holds does not reach an earlier query
+ * (infinities and NaN included).
+ *   q          query (b, i, h) at q + b*q_stride_b + i*q_stride_t + h*q_stride_h, as
+ *              nsn_extend_attention; n_queries 1 .. 128, own window 128.
+ *   out        device, out_dtype, [batch][n_queries][n_q_heads][128].
+ *   workspace  >= nsn_prefix_workspace_bytes(..., n_queries), as above; one that is large
+ *              enough for each serves calls of several n_queries, and decode calls, in turn.
+ * Everything else, rounding included, is as in nsn_decode_attention_prefix.  A sequence
+ * whose window holds fewer than n_queries > 1 tokens sets status bit 8 of k_cache->status;
+ * its first queries then see no window token.
+ */
+nsn_status nsn_extend_attention_prefix(const nsn_cache* prefix_k, const nsn_cache* prefix_v,
+                                       const nsn_cache* k_cache, const nsn_cache* v_cache, const void* q,
+                                       int dtype, int n_q_heads, int n_queries, int64_t q_stride_b,
+                                       int64_t q_stride_t, int64_t q_stride_h, float softmax_scale,
+                                       const float* cb_k, const float* cb_v, void* out, int out_dtype,
+                                       void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Pre-RoPE keys ([TS] Metodologia 4: NSN is applied to the keys BEFORE the rotary
  * position embedding).  The K cache then holds pre-RoPE keys -- both the quantized
  * part and the fp16 window, filled by the same nsn_quantize_kv* / append calls --

@@ -120,7 +120,7 @@ def test_readback_on_a_stream_and_in_a_graph():
 def test_readback_of_what_the_quantizer_wrote():
     # prefill, appends across a flush, then read back: each token within the quantizer's own error, the window exact
     B, T, H = 2, 500, 2
-    x = torch.randn((B, T + 40, H, 128), device="cuda", dtype=torch.bfloat16)
+    x = torch.randn((B, T + 40, H, 128), generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
     cb = tl.codebook(2)
     dcb = torch.from_numpy(cb).cuda()
     kc, vc = nsn.Cache(B, H, 640, 128, 2), nsn.Cache(B, H, 640, 128, 2)
@@ -132,6 +132,6 @@ def test_readback_of_what_the_quantizer_wrote():
     nsn.nsn_dequantize_kv(kc, out, dcb)
     check(kc, out, 0, cb, 2)
     nq = int(kc.n_quant[0, 0])
-    assert torch.equal(out[:, nq:], x[:, nq:].float())
+    assert torch.equal(out[:, nq:], x[:, nq:].half().float())     # the window holds fp16
     cos = torch.nn.functional.cosine_similarity(out[:, :nq], x[:, :nq].float(), dim=-1)
     assert float(cos.min()) > 0.8

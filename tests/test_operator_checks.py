@@ -1,4 +1,4 @@
-"""CPU checks of the argument validation of nsn_dequantize_kv: refused before any launch."""
+"""CPU checks of the argument validation of nsn_dequantize_kv and the shared-prefix attention: refused before any launch."""
 import ctypes
 
 import pytest
@@ -37,3 +37,47 @@ def test_readback_refuses_a_bad_cache(lib):
     assert lib.nsn_dequantize_kv(None, *args) == 1
     assert lib.nsn_dequantize_kv(ctypes.byref(cache(capacity=100)), *args) == 1
     assert lib.nsn_dequantize_kv(ctypes.byref(cache(window=64)), *args) == 2
+
+
+def prefix_call(lib, pk=None, pv=None, k=None, v=None, chunk=None, **change):
+    pk, pv = pk or cache(batch=1), pv or cache(batch=1, mode=1)
+    k, v = k or cache(), v or cache(mode=1)
+    a = dict(q=16, dtype=1, heads=8, sb=1024, st=1024, sh=128, scale=0.1, cbk=16, cbv=16, out=16, odt=1, ws=256,
+             bytes=1 << 40) | change
+    refs = [ctypes.byref(c) for c in (pk, pv, k, v)]
+    if chunk is None:
+        return lib.nsn_decode_attention_prefix(*refs, a["q"], a["dtype"], a["heads"], a["sb"], a["sh"], a["scale"], a["cbk"],
+                                               a["cbv"], a["out"], a["odt"], a["ws"], a["bytes"], None)
+    return lib.nsn_extend_attention_prefix(*refs, a["q"], a["dtype"], a["heads"], chunk, a["sb"], a["st"], a["sh"], a["scale"],
+                                           a["cbk"], a["cbv"], a["out"], a["odt"], a["ws"], a["bytes"], None)
+
+
+@pytest.mark.parametrize("chunk", [None, 4])
+@pytest.mark.parametrize("change,status", [
+    (dict(q=None), 1), (dict(q=18), 1), (dict(dtype=5), 1), (dict(odt=-1), 1), (dict(heads=7), 1), (dict(heads=0), 1),
+    (dict(heads=6), 2), (dict(heads=32), 2), (dict(sb=-1024), 1), (dict(sh=129), 1), (dict(cbk=None), 1), (dict(cbv=24), 1),
+    (dict(out=None), 1), (dict(out=40), 1), (dict(ws=None), 1), (dict(ws=128), 1), (dict(bytes=1000), 3),
+    (dict(scale=float("nan")), 1),
+    (dict(pk=cache(batch=2)), 1), (dict(pk=cache(batch=1, heads=4)), 1), (dict(pk=cache(batch=1, mode=1)), 1),
+    (dict(pk=cache(batch=1, dq=1)), 1), (dict(pv=cache(batch=1, mode=1, capacity=384)), 1), (dict(v=cache(mode=1, window=0)), 1),
+    (dict(v=cache(mode=2)), 1), (dict(k=cache(capacity=100)), 1), (dict(k=cache(window=64)), 2),
+])
+def test_prefix_arguments(lib, chunk, change, status):
+    assert prefix_call(lib, chunk=chunk, **change) == status
+
+
+def test_extend_prefix_chunk_and_window(lib):
+    assert prefix_call(lib, chunk=0) == 1
+    assert prefix_call(lib, chunk=129) == 1
+    assert prefix_call(lib, chunk=4, k=cache(window=0), v=cache(mode=1, window=0)) == 2
+
+
+def test_prefix_workspace_size(lib):
+    size = lambda k, heads, n, pk=None: lib.nsn_prefix_workspace_bytes(  # noqa: E731
+        ctypes.byref(pk or cache(batch=1)), ctypes.byref(k), heads, n)
+    assert size(cache(), 8, 1) > 0
+    assert size(cache(), 8, 128) > size(cache(), 8, 1)
+    assert size(cache(batch=64), 8, 1) > size(cache(), 8, 1)
+    assert size(cache(), 7, 1) == 0 and size(cache(), 8, 0) == 0 and size(cache(), 8, 129) == 0
+    assert size(cache(), 8, 1, cache(batch=2)) == 0
+    assert size(cache(batch=1 << 24), 16, 128) == 0     # rows past what 32-bit counts allow
