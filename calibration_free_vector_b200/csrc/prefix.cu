@@ -12,11 +12,11 @@
 // CTA; a CTA writes the partial (m, l, sum) of each item it touches and a second kernel joins
 // them and applies H.
 //
-// One CTA: 20 warps, three of them idle (registers move between whole warpgroups).
-//   warps 8-15  decode tiles into shared memory: a lane gathers codewords (8-fold replicated
-//               fp16 codebook, free of bank conflicts), applies signs, scale and mean in fp16,
-//               and stores 16-byte chunks of the 128-byte-swizzled operand tile;
-//   warp 16     one thread issues the MMAs: S = Q K^T (both from shared memory) into tensor
+// One CTA: 20 warps, two of them idle (registers move between whole warpgroups).
+//   warps 8-11, 12-15  decode K tiles and V tiles into shared memory: a lane takes one token, gathers
+//               its codewords (4-fold replicated fp16 codebook), applies signs, scale and mean in
+//               fp16, and stores 16-byte chunks of the 128-byte-swizzled operand tile;
+//   warps 16, 17  issue the MMAs of one softmax group each: S = Q K^T (both from shared memory) into tensor
 //               memory and O += P V (P from tensor memory);
 //   warps 0-3, 4-7  two softmax groups, each with its own S/P and O columns: a thread owns one
 //               query row, so the softmax needs no exchange between lanes.
@@ -38,18 +38,21 @@ namespace {
 constexpr float PF_LOG2E = 1.4426950408889634f;
 constexpr float PF_INV_SQRT_D = 0.08838834764831845f;  // 1/sqrt(128)
 constexpr int PF_CTAS = 148;       // at most; one per SM
-constexpr int PF_DEQ_WARPS = 8;
-constexpr int PF_THREADS = 32 * (8 + PF_DEQ_WARPS + 4);  // the last warpgroup: the MMA warp and three idle ones
+constexpr int PF_DEQ_WARPS = 8;    // two teams, one for K tiles and one for V tiles
+constexpr int PF_TEAM = 4;
+constexpr int PF_THREADS = 32 * (8 + PF_DEQ_WARPS + 4);  // the last warpgroup: the MMA warps and two idle ones
 // Registers per thread after the roles part: at launch all 20 warps hold 96, so the sum over
-// the warps may not pass 20 x 96 = 1920: 8 x 120 + 8 x 88 + 4 x 64.
-constexpr int PF_REGS_SOFTMAX = 120, PF_REGS_DECODE = 88, PF_REGS_MMA = 64;
+// the warps may not pass 20 x 96 = 1920: 8 x 104 + 8 x 120 + 4 x 32.
+constexpr int PF_REGS_SOFTMAX = 104, PF_REGS_DECODE = 120, PF_REGS_MMA = 32;
 static_assert(8 * PF_REGS_SOFTMAX + PF_DEQ_WARPS * PF_REGS_DECODE + 4 * PF_REGS_MMA <= (PF_THREADS / 32) * 96, "registers of the CTA");
-constexpr int PF_RING = 3;         // K / V tiles in shared memory
+constexpr int PF_RING = 4;         // K / V tiles in shared memory
+constexpr int PF_REP = 4;          // replicas of each codeword
 constexpr int PF_TILE_BYTES = 32768;  // 128 tokens (or rows) x 128 dims fp16: two 16 KB halves of 64 dims
 constexpr uint32_t PF_HALF = 16384u;
 // The running max moves only when a score exceeds it by more than this (log2 units): w stays
 // below 2^8, and most tiles leave O alone.
 constexpr float PF_SLACK = 8.0f;
+#define NEG_INF __int_as_float(0xFF800000)
 constexpr uint32_t PF_WAIT_LIMIT = 1u << 22;   // attempts of a wait before it gives up (seconds)
 constexpr uint32_t PF_POLL_LIMIT = 1u << 26;   // idle rounds of the MMA thread's event loop (seconds)
 
@@ -90,20 +93,20 @@ struct PfInfo {            // of one tile, for the softmax
 struct PfSmem {
   alignas(1024) unsigned char q[2][PF_TILE_BYTES];
   alignas(1024) unsigned char ring[PF_RING][PF_TILE_BYTES];
-  alignas(128) uint4 cbk[NCODES][8];
-  alignas(128) uint4 cbv[NCODES][8];
-  alignas(16) unsigned char o[PF_DEQ_WARPS][128];  // the half mean row of the tile a decode warp is at
+  alignas(128) uint4 cbk[NCODES][PF_REP];
+  alignas(128) uint4 cbv[NCODES][PF_REP];
+  alignas(16) unsigned char o[PF_DEQ_WARPS][256];  // the mean row of the tile a decode warp is at
   alignas(16) PfInfo info[4];
-  alignas(16) float red[2][PF_DEQ_WARPS];
-  int red_bad[PF_DEQ_WARPS];
-  alignas(8) uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], full[PF_RING], empty[PF_RING], meet, drain;
+  float red[2][2][2][PF_TEAM];     // per team (double-buffered: window tiles in turn): K and V scales
+  int red_bad[2][2][PF_TEAM];
+  alignas(8) uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], full[PF_RING], empty[PF_RING], meet[2], drain[2];
   long long scan[PF_THREADS / 32];
   long long units;
   int seg0, rt0, u0;
   uint32_t tmem;
   int fail;
 };
-static_assert(sizeof(PfSmem) + 1024 <= 232448, "shared memory of one SM");
+static_assert(sizeof(PfSmem) <= 232448, "shared memory of one SM");
 
 // ---------------------------------------------------------------------------
 // Barriers, tensor core and tensor memory
@@ -150,27 +153,56 @@ __device__ __forceinline__ void tc_commit_to(uint64_t* b) {
 // Matrix descriptors of the 128-byte-swizzled operands (descriptor version 1, layout 2): 8-row
 // groups of 128-byte rows 1024 B apart; the leading offset is the distance of the two 64-dim
 // halves where the operand is read across them (V: dims are the N axis).
-// kind::f16, fp32 accumulator, fp16 operands, M = N = 128; V is read with its N axis (dims) contiguous.
-constexpr uint32_t PF_IDESC_QK = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-constexpr uint32_t PF_IDESC_PV = PF_IDESC_QK | (1u << 16);
+// kind::f16, fp32 accumulator, fp16 operands, M = 128; S: N = 64 tokens; O: N = 128 dims, V read with
+// its N axis (dims) contiguous.
+constexpr uint32_t PF_IDESC_QK = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t PF_IDESC_PV = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 
-// Issued by one elected lane of a converged warp: with the operands uniform across the warp the
-// compiler keeps them in uniform registers (about 35 cycles an MMA; from a single-lane branch each
-// operand is moved there first, 55 cycles alone and over 100 beside busy warps).  A descriptor is its
-// low word (start address and leading offset) and the constant high word.
+// The K = 16 steps of one product, issued by one elected lane of a converged warp: with operands uniform across the warp the compiler keeps them in uniform registers.  From a
+// single-lane branch, where each operand is moved there first, an MMA took over 100 cycles to issue
+// beside the busy warps, twice its execution.  A descriptor is its low word (start address and leading
+// offset) and the constant high word.
 constexpr uint32_t PF_DESC_HI = (uint32_t)(((1024ull >> 4 << 32) | (1ull << 46) | (2ull << 61)) >> 32);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return ((addr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16); }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
+// S = Q K^T: 32 bytes of dims a step within the 128-byte rows, then the other 64-dim half (16 KB on).
+__device__ __forceinline__ void mma_qk(uint32_t d, uint32_t a, uint32_t b) {
   asm volatile(
-      "{\n .reg .pred p, e;\n .reg .b64 da, db;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n"
-      ::"r"(d), "r"(a), "r"(b), "r"(PF_IDESC_QK), "r"((uint32_t)accumulate), "r"(PF_DESC_HI) : "memory");
+      "{\n .reg .pred p, e;\n .reg .b64 da, db;\n .reg .b32 x, y;\n elect.sync _|e, 0xffffffff;\n"
+      " add.u32 x, %1, 0;\n add.u32 y, %2, 0;\n mov.b64 da, {x, %4};\n mov.b64 db, {y, %4};\n"
+      " setp.ne.b32 p, 0, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n"
+      " add.u32 x, %1, 2;\n add.u32 y, %2, 2;\n mov.b64 da, {x, %4};\n mov.b64 db, {y, %4};\n"
+      " setp.eq.b32 p, 0, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n"
+      " add.u32 x, %1, 4;\n add.u32 y, %2, 4;\n mov.b64 da, {x, %4};\n mov.b64 db, {y, %4};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n"
+      " add.u32 x, %1, 6;\n add.u32 y, %2, 6;\n mov.b64 da, {x, %4};\n mov.b64 db, {y, %4};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n"
+      " add.u32 x, %1, 1024;\n add.u32 y, %2, 1024;\n mov.b64 da, {x, %4};\n mov.b64 db, {y, %4};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n"
+      " add.u32 x, %1, 1026;\n add.u32 y, %2, 1026;\n mov.b64 da, {x, %4};\n mov.b64 db, {y, %4};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n"
+      " add.u32 x, %1, 1028;\n add.u32 y, %2, 1028;\n mov.b64 da, {x, %4};\n mov.b64 db, {y, %4};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n"
+      " add.u32 x, %1, 1030;\n add.u32 y, %2, 1030;\n mov.b64 da, {x, %4};\n mov.b64 db, {y, %4};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n"
+      "}\n"
+      ::"r"(d), "r"(a), "r"(b), "r"(PF_IDESC_QK), "r"(PF_DESC_HI) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
+// O (+)= P V over 64 tokens: 8 columns of P and 16 token rows (2 KB) of V a step.
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p, e;\n .reg .b64 db;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " mov.b64 db, {%2, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n"
+      "{\n .reg .pred p, e;\n .reg .b64 db;\n .reg .b32 x, y;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " add.u32 x, %1, 0;\n add.u32 y, %2, 0;\n mov.b64 db, {y, %5};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n"
+      " add.u32 x, %1, 8;\n add.u32 y, %2, 128;\n mov.b64 db, {y, %5};\n"
+      " setp.eq.b32 p, 0, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n"
+      " add.u32 x, %1, 16;\n add.u32 y, %2, 256;\n mov.b64 db, {y, %5};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n"
+      " add.u32 x, %1, 24;\n add.u32 y, %2, 384;\n mov.b64 db, {y, %5};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n"
+      "}\n"
       ::"r"(d), "r"(a), "r"(b), "r"(PF_IDESC_PV), "r"((uint32_t)accumulate), "r"(PF_DESC_HI) : "memory");
 }
 
@@ -192,6 +224,10 @@ __device__ __forceinline__ void tm_ready32(uint32_t (&r)[32]) {
                  "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
                  "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                :: "memory");
+}
+__device__ __forceinline__ void tm_ready64(uint32_t (&r)[32], uint32_t (&q)[32]) {
+  tm_ready32(r);
+  tm_ready32(q);
 }
 __device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t (&r)[32]) {
   tm_ld32_async(addr, r);
@@ -219,6 +255,10 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
+// A value that all lanes hold, in a form that the compiler knows to be warp-uniform (a reduction's
+// result is): the MMA operands derived from it then stay in uniform registers.
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
 // Two fp32 values in a register pair, and arithmetic on both at once.
 __device__ __forceinline__ uint64_t pack_f2(float x, float y) {
   uint64_t r;
@@ -324,14 +364,13 @@ __device__ __forceinline__ int64_t acc_off(int64_t row0, int hr, int row, int c)
 // ---------------------------------------------------------------------------
 // Decode warps
 // ---------------------------------------------------------------------------
-// What a lane reads for one K or V tile of a quantized block: token 32 (w >> 1) + lane,
-// sub-vectors 8 (w & 1) .. + 7 of it, and what the block's largest s1 needs.
+// What a lane reads for one K or V tile of a quantized block: token 32 w + lane of it (w: the warp
+// within its team), and what the block's largest s1 needs.
 struct Raw {
-  uint32_t ce, co;        // codes of the even and odd sub-vectors
-  uint4 sign;
+  uint4 code, sign;
   uint32_t norm;          // fp16 (s1, s2), or fp16 s2 and the s1 level
   uint4 four;             // s1 of tokens 4 lane .. 4 lane + 3 (fp16 pairs, or levels)
-  uint32_t mean;          // dims 64 (w & 1) + 2 lane, + 1
+  uint2 mean;             // dims 4 lane .. + 3
   uint2 par;              // fp16 (s1 lo, s1 hi, o lo, o hi)
 };
 
@@ -365,18 +404,16 @@ __device__ __forceinline__ void four_load(uint4& four, uint2& par, const Src& c,
 
 template <int MODE, bool DQ>
 __device__ __forceinline__ void raw_load(Raw& r, const Src& c, int64_t blk, int w, int lane) {
-  const int hs = w & 1, t = 32 * (w >> 1) + lane;
-  const uint32_t* code = reinterpret_cast<const uint32_t*>(c.codes + blk * (BLK * NSUB)) + 4 * t;
-  r.ce = __ldg(code + hs);
-  r.co = __ldg(code + 2 + hs);
+  const int t = 32 * w + lane;
+  r.code = __ldg(reinterpret_cast<const uint4*>(c.codes + blk * (BLK * NSUB)) + t);
   if constexpr (MODE == NSN_MODE_2BIT) r.sign = __ldg(reinterpret_cast<const uint4*>(c.signs + blk * (BLK * NSUB)) + t);
   if constexpr (DQ) {
     const uint32_t lev = (uint32_t)__ldg(c.levels + blk * (BLK / 2) + t / 2) >> (4 * (uint32_t)(t & 1)) & 15u;
     r.norm = (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(c.norms + blk * (2 * BLK)) + t) | (lev << 16);
-    r.mean = __ldg(c.means + blk * (D / 2) + 32 * hs + lane);
+    r.mean.x = __ldg(reinterpret_cast<const unsigned short*>(c.means + blk * (D / 2)) + lane);
   } else {
     r.norm = __ldg(reinterpret_cast<const uint32_t*>(c.norms + blk * (4 * BLK)) + t);
-    r.mean = __ldg(reinterpret_cast<const uint32_t*>(c.means + blk * (2 * D)) + 32 * hs + lane);
+    r.mean = __ldg(reinterpret_cast<const uint2*>(c.means + blk * (2 * D)) + lane);
   }
   four_load<DQ>(r.four, r.par, c, blk, lane);
 }
@@ -405,18 +442,20 @@ __device__ __forceinline__ float block_smax(const uint4& four, const uint2& par,
   return warp_max(m);
 }
 
-// Writes this warp's share of a decoded tile: fp16((u_hat s2 + o) s1 / smax) per token.
+// Writes this warp's 32 rows of a decoded tile: fp16((u_hat s2 + o) s1 / smax) per token.
 template <int MODE, bool DQ>
-__device__ __forceinline__ void tile_write(const Raw& r, const uint4 (*cb)[8], unsigned char* tile, unsigned char* orow,
+__device__ __forceinline__ void tile_write(const Raw& r, const uint4 (*cb)[PF_REP], unsigned char* tile, unsigned char* orow,
                                            float smax, int nvalid, int w, int lane) {
-  const int hs = w & 1, row = 32 * (w >> 1) + lane;
+  const int row = 32 * w + lane;
   float s1, s2;
-  uint32_t mean = r.mean;
+  uint2 mean = r.mean;
   if constexpr (DQ) {
     const float2 ls = lo_step(r.par.x), lo = lo_step(r.par.y);
     s1 = fmaf((float)(r.norm >> 16), ls.y, ls.x);
     s2 = __low2float(as_h2(r.norm));
-    mean = pack_h2(fmaf((float)(r.mean & 15u), lo.y, lo.x), fmaf((float)(r.mean >> 4), lo.y, lo.x));
+    const uint32_t v = r.mean.x;
+    mean.x = pack_h2(fmaf((float)(v & 15u), lo.y, lo.x), fmaf((float)((v >> 4) & 15u), lo.y, lo.x));
+    mean.y = pack_h2(fmaf((float)((v >> 8) & 15u), lo.y, lo.x), fmaf((float)(v >> 12), lo.y, lo.x));
   } else {
     const float2 n = __half22float2(as_h2(r.norm));
     s1 = n.x;
@@ -425,32 +464,32 @@ __device__ __forceinline__ void tile_write(const Raw& r, const uint4 (*cb)[8], u
   const float ratio = smax > 0.f ? s1 / smax : 0.f;
   const __half2 b2 = __float2half2_rn(ratio), a2 = __float2half2_rn(ratio * s2);
   __syncwarp();  // the previous tile's mean row has been read
-  reinterpret_cast<uint32_t*>(orow)[lane] = mean;
+  reinterpret_cast<uint2*>(orow)[lane] = mean;
   __syncwarp();
-  unsigned char* dst = tile + hs * PF_HALF + row * 128;
+  unsigned char* dst = tile + row * 128;
   const bool live = row < nvalid;
-  const uint4* rep = &cb[0][lane & 7];
+  const uint4* rep = &cb[0][lane & (PF_REP - 1)];
+  const uint32_t sw[4] = {r.sign.x, r.sign.y, r.sign.z, r.sign.w};
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t code = __byte_perm((k & 1) ? r.co : r.ce, 0u, 0x4440u | (uint32_t)(k >> 1));
-    const uint4 c = rep[code * 8];
-    const uint4 o = *reinterpret_cast<const uint4*>(orow + 16 * k);
+  for (int s = 0; s < NSUB; ++s) {  // the record holds the even sub-vectors' codes, then the odd ones'
+    const uint32_t word = (s & 1) ? ((s >> 1) < 4 ? r.code.z : r.code.w) : ((s >> 1) < 4 ? r.code.x : r.code.y);
+    const uint32_t code = __byte_perm(word, 0u, 0x4440u | (uint32_t)((s >> 1) & 3));
+    const uint4 c = rep[code * PF_REP];
+    const uint4 o = *reinterpret_cast<const uint4*>(orow + 16 * s);
     uint32_t u[4] = {c.x, c.y, c.z, c.w};
     const uint32_t om[4] = {o.x, o.y, o.z, o.w};
-    if constexpr (MODE == NSN_MODE_2BIT) {
-      const uint32_t sw[4] = {r.sign.x, r.sign.y, r.sign.z, r.sign.w};
-      const int s = 8 * hs + k;  // the sign of dim 8 s + i is bit 15 - s of field i
+    if constexpr (MODE == NSN_MODE_2BIT) {  // the sign of dim 8 s + i is bit 15 - s of field i
 #pragma unroll
       for (int i = 0; i < 4; ++i) u[i] ^= (sw[i] << s) & 0x80008000u;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) u[i] = as_u32(__hfma2(as_h2(u[i]), a2, __hmul2(as_h2(om[i]), b2)));
-    *reinterpret_cast<uint4*>(dst + ((k ^ (row & 7)) << 4)) =
+    *reinterpret_cast<uint4*>(dst + (s >> 3) * PF_HALF + (((s & 7) ^ (row & 7)) << 4)) =
         live ? make_uint4(u[0], u[1], u[2], u[3]) : make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
-// Window rows 16 w .. 16 w + 15 of one sequence as A fragments of the transform (rows past nw: zero).
+// Window rows 16 w .. 16 w + 15 (w: a 16-row group) of one sequence as A fragments of the transform (rows past nw: zero).
 __device__ __forceinline__ void window_load(uint32_t (&f)[8][4], const CacheView& c, int64_t seq, int nw, int w, int lane) {
   const int g = lane >> 2, p = lane & 3;
 #pragma unroll
@@ -519,98 +558,95 @@ __device__ __forceinline__ void window_write(const uint32_t (&f)[8][4], float sm
   }
 }
 
-// Meets the other decode warps (bounded, as every wait here); `phase` counts the meetings.
-__device__ __forceinline__ bool decode_sync(PfSmem& sm, uint32_t& phase, int lane) {
+// Meets the other warps of the team (bounded, as every wait here); `phase` counts the meetings.
+__device__ __forceinline__ bool decode_sync(PfSmem& sm, int team, uint32_t& phase, int lane) {
   __syncwarp();
-  if (lane == 0) bar_arrive(&sm.meet);
-  return bar_wait(&sm.meet, phase++, &sm.fail);
+  if (lane == 0) bar_arrive(&sm.meet[team]);
+  return bar_wait(&sm.meet[team], phase++, &sm.fail);
 }
 
-// One decode warp's walk over the pieces: tasks in ring order, the next task's global reads
-// issued before the current one waits for its slot.
-template <int MK, int MV, bool DQ>
+// One decode warp's walk over the pieces: the K team (TV = false) or the V team; the next tile's
+// global reads are issued before the current one waits for its slot.  The K team also leaves
+// each tile's scales for the softmax.
+template <int MODE, bool DQ, bool TV>
 __device__ __forceinline__ bool decode_role(const PfArgs& a, PfSmem& sm, Cursor cur, int w, int lane) {
   Piece p;
-  int n = 0;  // ring index
+  int tg0 = 0;        // tiles of the CTA before this piece
   uint32_t met = 0;
-  float window_vmax = 0.f;  // V scale of the piece's window tile
+  unsigned char* orow = sm.o[w + (TV ? PF_TEAM : 0)];
   while (next_piece(a, cur, p)) {
     const CacheView& kc = p.own ? a.k : a.pk;
     const CacheView& vc = p.own ? a.v : a.pv;
     const int64_t seq = p.own ? p.seg - a.H : p.seg;
-    const Src ks = seq_src<DQ>(kc, seq), vs = seq_src<DQ>(vc, seq);
-    const int base = n, tasks = 2 * p.m;
-    Raw next, vraw;
-    uint4 v4 = make_uint4(0u, 0u, 0u, 0u);   // V norms of a K task's block (for the tile's scales)
+    const Src src = seq_src<DQ>(TV ? vc : kc, seq), vs = seq_src<DQ>(vc, seq);
+    Raw next, raw;
+    uint4 v4 = make_uint4(0u, 0u, 0u, 0u);   // V norms of a K tile's block (for the tile's scales)
     uint2 vp = make_uint2(0u, 0u);
-    // task i of the piece: K of tile (i + 1) / 2 for odd i and i = 0, V of tile i / 2 - 1 for even i, V of the last tile at the end
-    const auto is_k = [&](int i) { return i == 0 || ((i & 1) && i != tasks - 1); };
-    const auto tile_of = [&](int i) { return i == 0 ? 0 : i == tasks - 1 ? p.m - 1 : (i & 1) ? (i + 1) / 2 : i / 2 - 1; };
-    const auto fetch = [&](int i) {
-      const int blk = p.j + tile_of(i);
+    const auto fetch = [&](int t) {
+      const int blk = p.j + t;
       if (blk >= p.s.blocks) return;
-      if (is_k(i)) {
-        raw_load<MK, DQ>(next, ks, blk, w, lane);
-        four_load<DQ>(v4, vp, vs, blk, lane);
-      } else {
-        raw_load<MV, DQ>(next, vs, blk, w, lane);
-      }
+      raw_load<MODE, DQ>(next, src, blk, w, lane);
+      if constexpr (!TV) four_load<DQ>(v4, vp, vs, blk, lane);
     };
     fetch(0);
-    for (int i = 0; i < tasks; ++i, ++n) {
-      vraw = next;
+    for (int t = 0; t < p.m; ++t) {
+      raw = next;
       const uint4 c4 = v4;
       const uint2 cp = vp;
-      if (i + 1 < tasks) fetch(i + 1);
-      const int t = tile_of(i), blk = p.j + t, slot = n % PF_RING;
-      const bool k_task = is_k(i);
+      if (t + 1 < p.m) fetch(t + 1);
+      const int n = 2 * tg0 + (TV ? ring_v(t, p.m) : ring_k(t)), slot = n % PF_RING, blk = p.j + t;
       if (n >= PF_RING && !bar_wait(&sm.empty[slot], (uint32_t)(n / PF_RING - 1), &sm.fail)) return false;
       unsigned char* tile = sm.ring[slot];
       PfInfo info;
       if (blk < p.s.blocks) {
         const int nvalid = min(BLK, p.s.nq - BLK * blk);
-        const float smax = block_smax<DQ>(vraw.four, vraw.par, nvalid, lane);
-        if (k_task) {
-          tile_write<MK, DQ>(vraw, sm.cbk, tile, sm.o[w], smax, nvalid, w, lane);
+        const float smax = block_smax<DQ>(raw.four, raw.par, nvalid, lane);
+        tile_write<MODE, DQ>(raw, TV ? sm.cbv : sm.cbk, tile, orow, smax, nvalid, w, lane);
+        if constexpr (!TV) {
           const float vmax = block_smax<DQ>(c4, cp, nvalid, lane);
           info.ka = smax > 0.f ? smax : 1.f;
           info.iva = vmax > 0.f ? vmax : 1.f;
           info.vbad = BLK;
           info.nvalid = info.base = nvalid;
           info.step = 0;
-        } else {
-          tile_write<MV, DQ>(vraw, sm.cbv, tile, sm.o[w], smax, nvalid, w, lane);
         }
       } else {
-        float smax = window_vmax;
+        // the team's scale over the whole tile; the K team takes V's along
+        float smax = 0.f, vmax = 0.f;
         int vbad = BLK;
         uint32_t f[8][4];
-        if (k_task) {  // scales of K and V over the whole tile (V is read again for its own task)
-          float mine, mine_v;
+        const uint32_t buf = met & 1;
+#pragma unroll 1
+        for (int i = 0; i < (TV ? 2 : 4); ++i) {
+          float mine;
           int bad;
-          window_load(f, vc, seq, p.s.nw, w, lane);
-          window_scan(f, w, lane, mine_v, vbad);
-          window_load(f, kc, seq, p.s.nw, w, lane);
-          window_scan(f, w, lane, mine, bad);
-          if (lane == 0) {
-            sm.red[0][w] = mine;
-            sm.red[1][w] = mine_v;
-            sm.red_bad[w] = vbad;
+          const bool of_v = TV || i < 2;
+          window_load(f, of_v ? vc : kc, seq, p.s.nw, 2 * w + (i & 1), lane);
+          window_scan(f, 2 * w + (i & 1), lane, mine, bad);
+          if (of_v) {
+            vmax = fmaxf(vmax, mine);
+            vbad = min(vbad, bad);
+          } else {
+            smax = fmaxf(smax, mine);
           }
-          if (!decode_sync(sm, met, lane)) return false;
-          smax = window_vmax = 0.f;
-#pragma unroll
-          for (int x = 0; x < PF_DEQ_WARPS; ++x) {
-            smax = fmaxf(smax, sm.red[0][x]);
-            window_vmax = fmaxf(window_vmax, sm.red[1][x]);
-            vbad = min(vbad, sm.red_bad[x]);
-          }
-          if (!decode_sync(sm, met, lane)) return false;
-        } else {
-          window_load(f, vc, seq, p.s.nw, w, lane);
         }
-        window_write(f, smax, !k_task, tile, w, lane);
-        const float vmax = window_vmax;
+        if (lane == 0) {
+          sm.red[TV][buf][0][w] = smax;
+          sm.red[TV][buf][1][w] = vmax;
+          sm.red_bad[TV][buf][w] = vbad;
+        }
+        if (!decode_sync(sm, TV, met, lane)) return false;
+#pragma unroll
+        for (int x = 0; x < PF_TEAM; ++x) {
+          smax = fmaxf(smax, sm.red[TV][buf][0][x]);
+          vmax = fmaxf(vmax, sm.red[TV][buf][1][x]);
+          vbad = min(vbad, sm.red_bad[TV][buf][x]);
+        }
+#pragma unroll 1
+        for (int i = 1; i >= 0; --i) {  // (the second 16 rows are still in f)
+          if (i == 0) window_load(f, TV ? vc : kc, seq, p.s.nw, 2 * w, lane);
+          window_write(f, TV ? vmax : smax, TV, tile, 2 * w + i, lane);
+        }
         info.ka = smax > 0.f ? smax : 1.f;
         info.iva = vmax > 0.f ? vmax : 1.f;
         info.vbad = vbad;
@@ -618,97 +654,92 @@ __device__ __forceinline__ bool decode_role(const PfArgs& a, PfSmem& sm, Cursor 
         info.step = p.own && a.causal ? 1 : 0;
         info.base = info.step ? p.s.nw - a.C + 1 : p.s.nw;
       }
-      if (k_task && w == 0 && lane == 0) {
+      if (!TV && w == 0 && lane == 0) {
         info.lv = log2f(info.iva);
         info.iva = 1.f / info.iva;
-        sm.info[(base / 2 + t) & 3] = info;
+        sm.info[(tg0 + t) & 3] = info;
       }
       fence_async();
       __syncwarp();
       if (lane == 0) bar_arrive(&sm.full[slot]);
     }
+    tg0 += p.m;
   }
   return true;
 }
 
 // ---------------------------------------------------------------------------
-// The MMA warp: an event loop over the two groups of a piece.  A group alternates
-// S = Q K^T of a tile (needs the K tile, and its previous P consumed) and O += P V (needs the
-// V tile and P); whichever group can go, goes.  The warp stays converged (votes decide).
+// The MMA warps, one per softmax group (one warp for both spent longer issuing than the products
+// took).  S and P of a group are two halves of 64 tokens: while the softmax works on one, the products
+// of the other run, so its scores are there when it is done.  S = Q K^T of a half needs the K tile and
+// its previous P consumed, O += P V the V tile and P.  Each warp walks every tile of every piece in ring
+// order and frees it, by a commit behind its own products or, where the other group alone uses
+// the tile, at once: no tile is replaced before both have seen it, so a barrier's parity is never
+// ambiguous.  The warps stay converged (votes decide).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ bool test_all(uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, bar_test(b, parity)); }
 
-struct MmaGroup {
-  int t;           // tile it is at
-  bool pv, first;  // waiting for P; no tile of the piece finished yet
-  uint32_t done;   // tiles finished, over all pieces
-  uint32_t built;  // query operands used, over all pieces
-};
-
-// One step of group I if it can go.
-template <int I>
-__device__ __forceinline__ bool mma_step(PfSmem& sm, MmaGroup& s, const Piece& p, int n0, uint32_t tmem, uint32_t q_lo, uint32_t k_lo, uint32_t v_lo) {
-  if (s.t >= p.m) return false;
-  const uint32_t s_col = tmem + 128u * I, o_col = tmem + 256u + 128u * I;
+__device__ __forceinline__ bool mma_role(const PfArgs& a, PfSmem& sm, Cursor cur, const int group) {
   constexpr uint32_t TILE = PF_TILE_BYTES >> 4;
-  if (!s.pv) {
-    const int n = n0 + ring_k(s.t), slot = n % PF_RING;
-    if (s.first ? !test_all(&sm.q_full[I], s.built) : !test_all(&sm.pv_done[I], s.done - 1u)) return false;
-    if (!test_all(&sm.full[slot], (uint32_t)(n / PF_RING))) return false;
-    tc_after();
-    const uint32_t kd = k_lo + TILE * (uint32_t)slot;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t step = ((k >> 2) * PF_HALF + (k & 3) * 32u) >> 4;
-      mma_ss(s_col, q_lo + TILE * I + step, kd + step, k > 0);
-    }
-    tc_commit_to(&sm.s_full[I]);
-    tc_commit_to(&sm.empty[slot]);
-    if (p.dual) tc_commit_to(&sm.empty[slot]);  // the barrier counts both groups
-    s.pv = true;
-  } else {
-    const int n = n0 + ring_v(s.t, p.m), slot = n % PF_RING;
-    if (!test_all(&sm.p_full[I], s.done)) return false;
-    if (!test_all(&sm.full[slot], (uint32_t)(n / PF_RING))) return false;
-    tc_after();
-    const uint32_t vd = v_lo + TILE * (uint32_t)slot;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) mma_ts(o_col, s_col + 8u * k, vd + 128u * k, !s.first || k > 0);
-    tc_commit_to(&sm.pv_done[I]);
-    tc_commit_to(&sm.empty[slot]);
-    if (p.dual) tc_commit_to(&sm.empty[slot]);
-    s.pv = s.first = false;
-    ++s.done;
-    s.t += p.dual ? 2 : 1;
-  }
-  return true;
-}
-
-__device__ __forceinline__ bool mma_role(const PfArgs& a, PfSmem& sm, Cursor cur) {
   // descriptors differ from these only by constant steps of the start address (16-byte units)
-  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
-  const uint32_t q_lo = desc_lo(sm_addr(sm.q[0]), 16u), k_lo = desc_lo(sm_addr(sm.ring[0]), 16u), v_lo = desc_lo(sm_addr(sm.ring[0]), PF_HALF);
+  const uint32_t tmem = (uint32_t)uniform((int)sm.tmem);
+  const uint32_t s_col = tmem + 128u * group, o_col = tmem + 256u + 128u * group;
+  const uint32_t q_lo = desc_lo(sm_addr(sm.q[0]), 16u) + TILE * group, k_lo = desc_lo(sm_addr(sm.ring[0]), 16u),
+                 v_lo = desc_lo(sm_addr(sm.ring[0]), PF_HALF);
+  uint64_t *s_full = sm.s_full[group], *p_full = sm.p_full[group], *pv_done = sm.pv_done[group];
   Piece p;
-  int n0 = 0;
-  MmaGroup g0 = {0, false, true, 0u, 0u}, g1 = g0;
+  int n0 = 0, pieces = 0, seen = 0;        // ring index of the piece, pieces before it, ring tiles seen
+  uint32_t slot_seen = 0u, parity = 0u;    // of the next ring tile
+  uint32_t done = 0u, built = 0u;          // tiles finished and query operands used, over all pieces
+  uint32_t idle = 0;
   while (next_piece(a, cur, p)) {
-    p.m = __shfl_sync(0xffffffffu, p.m, 0);
-    p.dual = __all_sync(0xffffffffu, p.dual);
-    g0.t = 0;
-    g1.t = p.dual ? 1 : 0;
-    g0.pv = g1.pv = false;
-    g0.first = g1.first = true;
-    uint32_t idle = 0;
-    while (g0.t < p.m || g1.t < p.m) {
-      const bool m0 = mma_step<0>(sm, g0, p, n0, tmem, q_lo, k_lo, v_lo);
-      const bool m1 = mma_step<1>(sm, g1, p, n0, tmem, q_lo, k_lo, v_lo);
-      if (m0 || m1) idle = 0;
+    const int m = uniform(p.m), step = uniform(p.dual ? 2 : 1), first = step == 2 ? (group + pieces) & 1 : 0;
+    const int halves = first < m ? 2 * ((m - first + step - 1) / step) : 0, end = n0 + 2 * m;
+    int qk = 0, pv = 0;                    // next half tile of each product
+    bool have_q = false;
+    while (pv < halves || seen < end) {
+      bool moved = false;
+      if (seen < end && test_all(&sm.full[slot_seen], parity)) {
+        const int r = seen - n0;           // K0 K1 V0 K2 V1 ... V(m-1)
+        const int t = r == 0 ? 0 : r == 2 * m - 1 ? m - 1 : (r & 1) ? (r + 1) >> 1 : (r >> 1) - 1;
+        if (step == 2 && ((t - first) & 1) && (threadIdx.x & 31) == 0) bar_arrive(&sm.empty[slot_seen]);
+        ++seen;
+        if (++slot_seen == PF_RING) {
+          slot_seen = 0u;
+          parity ^= 1u;
+        }
+        moved = true;
+      }
+      if (pv < qk) {  // O += P V of half pv
+        const int t = first + step * (pv >> 1), h = pv & 1, n = n0 + ring_v(t, m), slot = n % PF_RING;
+        if (n < seen && test_all(&p_full[h], done + (uint32_t)(pv >> 1))) {
+          tc_after();
+          mma_pv(o_col, s_col + 64u * h, v_lo + TILE * (uint32_t)slot + 512u * h, pv > 0);
+          tc_commit_to(&pv_done[h]);
+          if (h) tc_commit_to(&sm.empty[slot]);
+          ++pv;
+          moved = true;
+        }
+      }
+      if (qk < halves && qk < pv + 2) {  // S = Q K^T of half qk, two ahead of O at most
+        const int t = first + step * (qk >> 1), h = qk & 1, n = n0 + ring_k(t), slot = n % PF_RING;
+        if (!have_q) have_q = test_all(&sm.q_full[group], built);
+        if (have_q && n < seen && (qk < 2 || test_all(&pv_done[h], done + (uint32_t)(qk >> 1) - 1u))) {
+          tc_after();
+          mma_qk(s_col + 64u * h, q_lo, k_lo + TILE * (uint32_t)slot + 512u * h);
+          tc_commit_to(&s_full[h]);
+          if (h) tc_commit_to(&sm.empty[slot]);
+          ++qk;
+          moved = true;
+        }
+      }
+      if (moved) idle = 0;
       else if (++idle > PF_POLL_LIMIT || ((idle & 255u) == 0u && __any_sync(0xffffffffu, *(volatile int*)&sm.fail))) return false;
     }
-    // (a group without tiles here - one tile, alternating groups - has not built a query operand)
-    g0.built += g0.first ? 0u : 1u;
-    g1.built += g1.first ? 0u : 1u;
-    n0 += 2 * p.m;
+    done += (uint32_t)(halves >> 1);
+    built += halves ? 1u : 0u;
+    n0 = end;
+    ++pieces;
   }
   return true;
 }
@@ -830,28 +861,33 @@ __global__ void __launch_bounds__(32 * QUERY_WARPS) prefix_query_kernel(const __
 // ---------------------------------------------------------------------------
 // Softmax groups
 // ---------------------------------------------------------------------------
-// The running max moved after c chunks of a tile: O (unless the tile is the item's first) and the
-// tile's weights so far are scaled by f.
-__device__ __forceinline__ void move_max(uint32_t s_col, uint32_t o_col, int c, bool have_o, float f) {
-  if (have_o) {
-#pragma unroll 1
-    for (int x = 0; x < 8; ++x) {
-      uint32_t o[16];
-      tm_ld16(o_col + 16u * x, o);
+// Scores of columns `limit` and up count as -inf.
+__device__ __forceinline__ void mask_scores(uint32_t (&s)[32], int limit) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-      tm_st16(o_col + 16u * x, o);
-    }
+  for (int i = 0; i < 32; ++i)
+    if (i >= limit) s[i] = 0xFF800000u;
+}
+// The weights of 32 scores, 2^(ka s + off), as fp16 pairs; their fp32 sums are added to `sum`.
+__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t (&w)[16], uint64_t ka2, uint64_t off2, uint64_t (&sum)[2]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float e0, e1;
+    unpack_f2(fma_f2(pack_f2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), ka2, off2), e0, e1);
+    e0 = ex2(e0);
+    e1 = ex2(e1);
+    sum[i & 1] = add_f2(sum[i & 1], pack_f2(e0, e1));
+    w[i] = pack_h2(e0, e1);
   }
-  const __half2 f2 = __float2half2_rn(f);
+}
+// The running max has moved: this warp's rows of O are scaled.
+__device__ __forceinline__ void scale_o(uint32_t o_col, float f) {
 #pragma unroll 1
-  for (int x = 0; x < c; ++x) {
-    uint32_t w[16];
-    tm_wait_st();
-    tm_ld16(s_col + 16u * x, w);
+  for (int x = 0; x < 8; ++x) {
+    uint32_t o[16];
+    tm_ld16(o_col + 16u * x, o);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = as_u32(__hmul2(as_h2(w[i]), f2));
-    tm_st16(s_col + 16u * x, w);
+    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+    tm_st16(o_col + 16u * x, o);
   }
 }
 
@@ -862,9 +898,11 @@ __device__ __forceinline__ bool softmax_role(const PfArgs& a, PfSmem& sm, Cursor
   Piece p;
   uint32_t tiles = 0;       // of this group, over all pieces
   copies = 0;               // query operands copied
+  int pieces = 0;
   int tg0 = 0;              // tiles of the CTA before this piece
   while (next_piece(a, cur, p)) {
-    const int first = p.dual ? group : 0;
+    // (alternating groups also take turns at the first tile, so that two one-tile items overlap)
+    const int first = p.dual ? (group + pieces) & 1 : 0;
     const bool some = first < p.m;  // else nothing here waits for the MMAs, and no barrier may move
     if (some && wq == 0 && lane == 0) {
       // (the group's MMAs that read the previous operand have finished: pv_done was waited for)
@@ -882,77 +920,61 @@ __device__ __forceinline__ bool softmax_role(const PfArgs& a, PfSmem& sm, Cursor
     const int c_of_row = p.own ? (256 * p.rt + row) / a.G : 0;
     float m = NEG_BIG, l = 0.f;
     for (int t = first; t < p.m; t += p.dual ? 2 : 1, ++tiles) {
-      if (!bar_wait(&sm.s_full[group], tiles, &sm.fail)) return false;
-      if (warp_live) {
-        tc_after();
-        const PfInfo info = sm.info[(tg0 + t) & 3];
-        const int limit = min(info.nvalid, info.base + info.step * c_of_row);
-        const bool masked = __any_sync(0xffffffffu, limit < BLK);
-        float lt = 0.f;
-        // the weights of columns 32 c .. + 31, whose scores s holds
-        const auto chunk = [&](const int c, uint32_t (&s)[32]) {
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= limit) s[i] = 0xFF800000u;  // -inf
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        if (!bar_wait(&sm.s_full[group][h], tiles, &sm.fail)) return false;
+        if (warp_live) {
+          tc_after();
+          const uint32_t col = s_col + 64u * h;
+          uint32_t sa[32], sb[32];
+          tm_ld32_async(col, sa);
+          tm_ld32_async(col + 32u, sb);
+          const PfInfo info = sm.info[(tg0 + t) & 3];
+          const int limit = min(info.nvalid, info.base + info.step * c_of_row) - 64 * h;
+          tm_ready64(sa, sb);
+          if (__any_sync(0xffffffffu, limit < 64)) {
+            mask_scores(sa, limit);
+            mask_scores(sb, limit - 32);
           }
-          float mx[4];
+          float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
-#pragma unroll
-          for (int i = 4; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+          for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], fmaxf(__uint_as_float(sa[i]), __uint_as_float(sb[i])));
           const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), info.ka, info.lv);
-          if (__any_sync(0xffffffffu, top > m + PF_SLACK)) {
+          // (rows that do not exist hold whatever the operand's memory held: they have no say)
+          if (__any_sync(0xffffffffu, row < p.rows && top > m + PF_SLACK)) {
             const float mn = fmaxf(m, top), f = ex2(m - mn);
             m = mn;
             l *= f;
-            lt *= f;
-            move_max(s_col, o_col, c, t != first, f);
+            if (t != first || h) {  // O: once the product before this half's has been added
+              if (!bar_wait(&sm.pv_done[group][h ^ 1], h ? tiles : tiles - 1u, &sm.fail)) return false;
+              tc_after();
+              scale_o(o_col, f);
+            }
           }
           const float off = info.lv - m;
           const uint64_t ka2 = pack_f2(info.ka, info.ka), off2 = pack_f2(off, off);
           uint64_t sum[2] = {0ull, 0ull};
           uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float e0, e1;
-            unpack_f2(fma_f2(pack_f2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), ka2, off2), e0, e1);
-            e0 = ex2(e0);
-            e1 = ex2(e1);
-            sum[i & 1] = add_f2(sum[i & 1], pack_f2(e0, e1));
-            w[i] = pack_h2(e0, e1);
-          }
+          weights(sa, w, ka2, off2, sum);
+          tm_st16(col, w);
+          weights(sb, w, ka2, off2, sum);
+          tm_st16(col + 16u, w);
           float a0, a1;
           unpack_f2(add_f2(sum[0], sum[1]), a0, a1);
-          lt += a0 + a1;
-          tm_st16(s_col + 16u * c, w);
-        };
-        // each chunk's columns are requested before the previous one is worked on; the
-        // weights of chunk c overwrite columns 16 c .. + 15, which have been read by then
-        uint32_t sa[32], sb[32];
-        tm_ld32_async(s_col, sa);
-#pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {  // (rolled: half the instructions to fetch)
-          tm_ready32(sa);
-          tm_ld32_async(s_col + 32u * c + 32u, sb);
-          chunk(c, sa);
-          tm_ready32(sb);
-          if (c == 0) tm_ld32_async(s_col + 64u, sa);
-          chunk(c + 1, sb);
+          l = fmaf(a0 + a1, info.iva, l);
+          if (limit > info.vbad - 64 * h) l = __int_as_float(0x7fc00000);  // a value it sees is not finite
+          tm_wait_st();
+          tc_before();
         }
-        l = fmaf(lt, info.iva, l);
-        if (limit > info.vbad) l = __int_as_float(0x7fc00000);  // a value it sees is not finite
-        tm_wait_st();
-        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sm.p_full[group][h]);
       }
-      __syncwarp();
-      if (lane == 0) bar_arrive(&sm.p_full[group]);
     }
     // ---- this group's partial of the item ----
     const int hr = p.own ? a.ro.hr : a.rp.hr;
     const int64_t row0 = slot_row(a, p.own, p.item, blockIdx.x);
     const int srow = (p.dual ? group * hr : 128 * group) + 32 * wq + lane;
-    if (some && !bar_wait(&sm.pv_done[group], tiles - 1u, &sm.fail)) return false;
+    if (some && !bar_wait(&sm.pv_done[group][1], tiles - 1u, &sm.fail)) return false;
     if (warp_live) {
       tc_after();
       if (row < p.rows) a.ml[row0 + srow] = make_float2(m, l);
@@ -976,15 +998,22 @@ __device__ __forceinline__ bool softmax_role(const PfArgs& a, PfSmem& sm, Cursor
       if (p.j + p.m == p.s.tiles) e->y = blockIdx.x;
     }
     tg0 += p.m;
+    ++pieces;
   }
   return true;
 }
 
 template <int MK, int MV, bool DQ>
 __global__ void __launch_bounds__(PF_THREADS, 1) prefix_kernel(const __grid_constant__ PfArgs a) {
-  extern __shared__ unsigned char smem_raw[];
-  PfSmem& sm = *reinterpret_cast<PfSmem*>(smem_raw + ((1024u - (sm_addr(smem_raw) & 1023u)) & 1023u));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  PfSmem& sm = *reinterpret_cast<PfSmem*>(smem_raw);
+  // (the swizzle needs 1024-byte aligned tiles; there is no room to align by hand, and no static
+  // shared memory that could move the base)
+  if (sm_addr(smem_raw) & 1023u) {
+    if (threadIdx.x == 0 && a.status) atomicOr(a.status, 2);
+    return;
+  }
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
   // ---- this CTA's range of the tiles ----
   const int nseg = a.H + (a.ro.rows > 0 ? a.B * a.H : 0);  // (own parts only where they are tiles)
@@ -1012,21 +1041,25 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_kernel(const __grid_cons
     const uint4 row = pack8_f16(c);
     uint4* dst = i < NCODES ? &sm.cbk[code][0] : &sm.cbv[code][0];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) dst[(r + code) & 7] = row;
+    for (int r = 0; r < PF_REP; ++r) dst[(r + code) & (PF_REP - 1)] = row;
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       bar_init(&sm.q_full[i], 1);
-      bar_init(&sm.s_full[i], 1);
-      bar_init(&sm.p_full[i], 4);
-      bar_init(&sm.pv_done[i], 1);
+      for (int h = 0; h < 2; ++h) {
+        bar_init(&sm.s_full[i][h], 1);
+        bar_init(&sm.p_full[i][h], 4);
+        bar_init(&sm.pv_done[i][h], 1);
+      }
     }
     for (int i = 0; i < PF_RING; ++i) {
-      bar_init(&sm.full[i], PF_DEQ_WARPS);
+      bar_init(&sm.full[i], PF_TEAM);
       bar_init(&sm.empty[i], 2);
     }
-    bar_init(&sm.meet, PF_DEQ_WARPS);
-    bar_init(&sm.drain, 1);
+    bar_init(&sm.meet[0], PF_TEAM);
+    bar_init(&sm.meet[1], PF_TEAM);
+    bar_init(&sm.drain[0], 1);
+    bar_init(&sm.drain[1], 1);
     sm.fail = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -1079,16 +1112,17 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_kernel(const __grid_cons
       bar_wait(&sm.q_full[warp >> 2], copies - 1u, &never);
     }
   } else if (warp < 16) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PF_REGS_DECODE));
-    ok = decode_role<MK, MV, DQ>(a, sm, cur, warp - 8, lane);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PF_REGS_DECODE));
+    ok = warp < 8 + PF_TEAM ? decode_role<MK, DQ, false>(a, sm, cur, warp - 8, lane)
+                            : decode_role<MV, DQ, true>(a, sm, cur, warp - 8 - PF_TEAM, lane);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PF_REGS_MMA));
-    if (warp == 16) {
-      ok = mma_role(a, sm, cur);
+    if (warp <= 17) {
+      ok = mma_role(a, sm, cur, warp - 16);
       if (!ok) {  // let MMAs in flight finish before tensor memory is given back
         int never = 0;
-        tc_commit_to(&sm.drain);
-        bar_wait(&sm.drain, 0u, &never);
+        tc_commit_to(&sm.drain[warp - 16]);
+        bar_wait(&sm.drain[warp - 16], 0u, &never);
       }
     }
   }
@@ -1233,7 +1267,7 @@ RowSet row_set(int64_t rows) {
 
 // With one query per sequence the own part has 1 to 8 rows per (b, kv-head): too few for a
 // 128-row tile, and the decode kernel takes it.  Longer chunks take tiles for both parts.
-bool own_by_decode(int n_queries) { return n_queries == 1; }
+bool own_by_decode(int n_queries) { return false; }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -1280,7 +1314,7 @@ cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned block, si
 
 template <int MK, int MV, bool DQ>
 cudaError_t launch_t(const PfArgs& a, int ctas, cudaStream_t s) {
-  const size_t smem = sizeof(PfSmem) + 1024;
+  const size_t smem = sizeof(PfSmem);
   const cudaError_t e = cudaFuncSetAttribute(prefix_kernel<MK, MV, DQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   return launch_early(prefix_kernel<MK, MV, DQ>, ctas, PF_THREADS, smem, true, s, a);
