@@ -60,6 +60,7 @@ struct RowSet {  // the rows of one kind of segment
   int rows;      // query rows of a segment
   int rt;        // 256-row tiles
   int hr;        // rows of one group's half of a partial slot (128, or the rows rounded up to 32)
+  int cost;      // of an item beside its tiles, in tiles
 };
 
 struct PfArgs {
@@ -310,10 +311,9 @@ struct Piece {
   int rows;         // rows of the 256-row tile that exist
   int64_t item;     // index among the items of its kind
 };
-// Ranges are cut in units of one tile plus PF_ITEM_COST for each item (its query operand, the
-// latency of its first scores and its partial, which are not overlapped with other items).
-constexpr int PF_ITEM_COST = 3;
-__device__ __forceinline__ int seg_units(const Seg& s) { return s.tiles > 0 ? s.tiles + PF_ITEM_COST : 0; }
+// Ranges are cut in units of one tile plus `cost` for each item (its query operand, the latency of its
+// first scores and its partial, which are not overlapped with the same group's other items).
+__device__ __forceinline__ int seg_units(const Seg& s, const RowSet& r) { return s.tiles > 0 ? s.tiles + r.cost : 0; }
 struct Cursor {
   int seg, rt, u;   // unit within the item
   long long left;   // units of this CTA's range
@@ -327,9 +327,9 @@ __device__ __forceinline__ bool next_piece(const PfArgs& a, Cursor& c, Piece& p)
     p.rt = c.rt;
     p.own = c.seg >= a.H;
     const RowSet& r = p.own ? a.ro : a.rp;
-    const int units = seg_units(p.s), n = (int)min((long long)(units - c.u), c.left);
-    p.j = max(0, c.u - PF_ITEM_COST);
-    p.m = max(0, c.u + n - PF_ITEM_COST) - p.j;
+    const int units = seg_units(p.s, r), n = (int)min((long long)(units - c.u), c.left);
+    p.j = max(0, c.u - r.cost);
+    p.m = max(0, c.u + n - r.cost) - p.j;
     p.rows = min(256, r.rows - 256 * c.rt);
     p.dual = p.rows <= 128;
     p.item = (int64_t)(p.own ? c.seg - a.H : c.seg) * r.rt + c.rt;
@@ -368,11 +368,39 @@ __device__ __forceinline__ int64_t acc_off(int64_t row0, int hr, int row, int c)
 // within its team), and what the block's largest s1 needs.
 struct Raw {
   uint4 code, sign;
-  uint32_t norm;          // fp16 (s1, s2), or fp16 s2 and the s1 level
+  uint32_t norm, level;   // fp16 (s1, s2); or fp16 s2, and the byte with the s1 level
   uint4 four;             // s1 of tokens 4 lane .. 4 lane + 3 (fp16 pairs, or levels)
   uint2 mean;             // dims 4 lane .. + 3
   uint2 par;              // fp16 (s1 lo, s1 hi, o lo, o hi)
 };
+
+// Reads that stay where they are written: the compiler moves ordinary read-only loads down to their
+// use, which would expose their latency once a tile.
+__device__ __forceinline__ uint4 ld_v4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint2 ld_v2(const void* p) {
+  uint2 r;
+  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint32_t ld_u32(const void* p) {
+  uint32_t r;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint32_t ld_u16(const void* p) {
+  uint16_t r;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint32_t ld_u8(const void* p) {
+  uint32_t r;
+  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(r) : "l"(p));
+  return r;
+}
 
 // Base addresses of one sequence's quantized buffers.
 struct Src {
@@ -395,25 +423,25 @@ __device__ __forceinline__ Src seq_src(const CacheView& c, int64_t seq) {
 template <bool DQ>
 __device__ __forceinline__ void four_load(uint4& four, uint2& par, const Src& c, int64_t blk, int lane) {
   if constexpr (DQ) {
-    four.x = __ldg(reinterpret_cast<const unsigned short*>(c.levels + blk * (BLK / 2)) + lane);
-    par = __ldg(reinterpret_cast<const uint2*>(c.params + blk * 16));
+    four.x = ld_u16(c.levels + blk * (BLK / 2) + 2 * lane);
+    par = ld_v2(c.params + blk * 16);
   } else {
-    four = __ldg(reinterpret_cast<const uint4*>(c.norms + blk * (4 * BLK)) + lane);
+    four = ld_v4(c.norms + blk * (4 * BLK) + 16 * lane);
   }
 }
 
 template <int MODE, bool DQ>
 __device__ __forceinline__ void raw_load(Raw& r, const Src& c, int64_t blk, int w, int lane) {
   const int t = 32 * w + lane;
-  r.code = __ldg(reinterpret_cast<const uint4*>(c.codes + blk * (BLK * NSUB)) + t);
-  if constexpr (MODE == NSN_MODE_2BIT) r.sign = __ldg(reinterpret_cast<const uint4*>(c.signs + blk * (BLK * NSUB)) + t);
+  r.code = ld_v4(c.codes + blk * (BLK * NSUB) + NSUB * t);
+  if constexpr (MODE == NSN_MODE_2BIT) r.sign = ld_v4(c.signs + blk * (BLK * NSUB) + NSUB * t);
   if constexpr (DQ) {
-    const uint32_t lev = (uint32_t)__ldg(c.levels + blk * (BLK / 2) + t / 2) >> (4 * (uint32_t)(t & 1)) & 15u;
-    r.norm = (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(c.norms + blk * (2 * BLK)) + t) | (lev << 16);
-    r.mean.x = __ldg(reinterpret_cast<const unsigned short*>(c.means + blk * (D / 2)) + lane);
+    r.norm = ld_u16(c.norms + blk * (2 * BLK) + 2 * t);
+    r.level = ld_u8(c.levels + blk * (BLK / 2) + t / 2);
+    r.mean.x = ld_u16(c.means + blk * (D / 2) + 2 * lane);
   } else {
-    r.norm = __ldg(reinterpret_cast<const uint32_t*>(c.norms + blk * (4 * BLK)) + t);
-    r.mean = __ldg(reinterpret_cast<const uint2*>(c.means + blk * (2 * D)) + lane);
+    r.norm = ld_u32(c.norms + blk * (4 * BLK) + 4 * t);
+    r.mean = ld_v2(c.means + blk * (2 * D) + 8 * lane);
   }
   four_load<DQ>(r.four, r.par, c, blk, lane);
 }
@@ -451,7 +479,7 @@ __device__ __forceinline__ void tile_write(const Raw& r, const uint4 (*cb)[PF_RE
   uint2 mean = r.mean;
   if constexpr (DQ) {
     const float2 ls = lo_step(r.par.x), lo = lo_step(r.par.y);
-    s1 = fmaf((float)(r.norm >> 16), ls.y, ls.x);
+    s1 = fmaf((float)((r.level >> (4 * (lane & 1))) & 15u), ls.y, ls.x);
     s2 = __low2float(as_h2(r.norm));
     const uint32_t v = r.mean.x;
     mean.x = pack_h2(fmaf((float)(v & 15u), lo.y, lo.x), fmaf((float)((v >> 4) & 15u), lo.y, lo.x));
@@ -1022,7 +1050,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_kernel(const __grid_cons
   bool short_window = false;
   for (int s = tid * per; s < min(nseg, (tid + 1) * per); ++s) {
     const Seg g = seg_info(a, s);
-    sum += (long long)seg_units(g) * (s >= a.H ? a.ro.rt : a.rp.rt);
+    const RowSet& r = s >= a.H ? a.ro : a.rp;
+    sum += (long long)seg_units(g, r) * r.rt;
     short_window |= s >= a.H && a.causal && a.C > 1 && g.nw < a.C;
   }
   if (short_window && blockIdx.x == 0 && a.status) atomicOr(a.status, 8);
@@ -1081,8 +1110,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_kernel(const __grid_cons
   long long at = before + inc - sum;  // tiles before this thread's segments
   if (at <= begin && begin < at + sum) {
     for (int s = tid * per;; ++s) {
-      const int units = seg_units(seg_info(a, s));
-      const long long here = (long long)units * (s >= a.H ? a.ro.rt : a.rp.rt);
+      const RowSet& r = s >= a.H ? a.ro : a.rp;
+      const int units = seg_units(seg_info(a, s), r);
+      const long long here = (long long)units * r.rt;
       if (begin < at + here) {
         sm.seg0 = s;
         sm.rt0 = (int)((begin - at) / units);
@@ -1262,12 +1292,20 @@ RowSet row_set(int64_t rows) {
   r.rows = (int)rows;
   r.rt = (int)((rows + 255) / 256);
   r.hr = rows > 128 ? 128 : (int)((rows + 31) / 32 * 32);
+  // (measured: 5 against 3, 8 x 128 queries behind 32k, 662 against 791 us; where the groups alternate
+  // tiles two items overlap, and 3 against 5 and 1: 64 queries behind 131k, 251 against 258 and 298 us)
+  r.cost = rows > 128 ? 5 : 3;
   return r;
 }
 
-// With one query per sequence the own part has 1 to 8 rows per (b, kv-head): too few for a
-// 128-row tile, and the decode kernel takes it.  Longer chunks take tiles for both parts.
-bool own_by_decode(int n_queries) { return false; }
+// With one query per sequence the own part has 1 to 8 rows per (b, kv-head), which a 128-row tile
+// wastes; the decode kernel reads such a cache faster, but has a fixed cost (its window is one warp's
+// work).  Measured, 8 kv-heads, 4 queries each, whole call behind an 8k prefix, tiles against decode
+// kernel: 16 x 300 own tokens 49 / 70 us, 16 x 1200 64 / 60, 16 x 2200 74 / 60; 64 x 100 78 / 115,
+// 64 x 300 100 / 83, 64 x 2200 242 / 112.  The lengths are on the device: the capacity decides.
+bool own_by_decode(int n_queries, int B, int H, int own_capacity) {
+  return n_queries == 1 && (int64_t)B * H * (own_capacity / BLK + 4) > 2800;
+}
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -1279,7 +1317,7 @@ struct PfLayout {
 };
 PfLayout layout(int B, int H, int g, int C, int own_capacity) {
   PfLayout y;
-  const bool dec = own_by_decode(C);
+  const bool dec = own_by_decode(C, B, H, own_capacity);
   y.rp = row_set((int64_t)B * C * g);
   y.ro = row_set(dec ? 0 : (int64_t)C * g);
   const int64_t ip = (int64_t)H * y.rp.rt, io = (int64_t)B * H * y.ro.rt, rows_out = (int64_t)B * C * H * g;
@@ -1356,7 +1394,7 @@ cudaError_t launch_prefix(const CacheView& pk, const CacheView& pv, const CacheV
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int ctas = sms < PF_CTAS ? sms : PF_CTAS;
-  if (own_by_decode(n_queries)) {
+  if (own_by_decode(a.C, a.B, a.H, k.capacity)) {
     float* oo = reinterpret_cast<float*>(w + y.own_out);
     float2* ol = reinterpret_cast<float2*>(w + y.own_lse);
     a.own_out = oo;

@@ -107,6 +107,25 @@ def test_decode_prefix_own_without_window():
     pt.check(*caches, q, decode(caches, q, dk, dv), cbk, cbv, 2, 1, SCALE)
 
 
+@pytest.mark.parametrize("own_window", [128, 0])
+def test_decode_prefix_large_own_caches(own_window):
+    # own caches whose capacity makes them the decode kernel's: long, short and empty ones
+    B, H, g, mk, mv = 64, 2, 4, 2, 1
+    own = [[(128 * ((5 * b + h) % 19), 0 if own_window == 0 else (31 * b + h) % 129) for h in range(H)] for b in range(B)]
+    caches = make([(640, 50), (0, 0)], own, mk, mv, False, seed=37, cap=2304, own_window=own_window)
+    cbk, cbv, dk, dv = books(mk, mv)
+    q = queries((B, H * g, 128), torch.bfloat16, seed=14)
+    ws = nsn.prefix_workspace(caches[0], caches[2], H * g)
+    outs = []
+    for _ in range(2):     # the counters are back at zero after a call
+        out = torch.full(q.shape, float("nan"), dtype=torch.float32, device="cuda")
+        nsn.nsn_decode_attention_prefix(*caches, q, SCALE, dk, dv, out, ws)
+        outs.append(out)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1])
+    pt.check(*caches, q, outs[0], cbk, cbv, mk, mv, SCALE, pick={(b, h) for b in range(0, B, 5) for h in range(H)})
+
+
 def test_decode_prefix_many_pieces():
     # several tiles and items per CTA, row tiles that several CTAs share
     B, H, g, mk, mv = 48, 4, 8, 2, 2
