@@ -374,34 +374,6 @@ struct Raw {
   uint2 par;              // fp16 (s1 lo, s1 hi, o lo, o hi)
 };
 
-// Reads that stay where they are written: the compiler moves ordinary read-only loads down to their
-// use, which would expose their latency once a tile.
-__device__ __forceinline__ uint4 ld_v4(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-  return r;
-}
-__device__ __forceinline__ uint2 ld_v2(const void* p) {
-  uint2 r;
-  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-  return r;
-}
-__device__ __forceinline__ uint32_t ld_u32(const void* p) {
-  uint32_t r;
-  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(p));
-  return r;
-}
-__device__ __forceinline__ uint32_t ld_u16(const void* p) {
-  uint16_t r;
-  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
-  return r;
-}
-__device__ __forceinline__ uint32_t ld_u8(const void* p) {
-  uint32_t r;
-  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(r) : "l"(p));
-  return r;
-}
-
 // Base addresses of one sequence's quantized buffers.
 struct Src {
   const unsigned char *codes, *signs, *norms, *means, *levels, *params;

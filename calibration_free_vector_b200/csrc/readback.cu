@@ -59,28 +59,25 @@ __device__ __forceinline__ void rb_store4(void* out, int64_t off, float a, float
 struct RbTile {
   uint2 code;
   uint32_t sign[2];
-  float s1[2], s2[2];
+  uint32_t norm[2], level[2];  // fp16 (s1, s2); or fp16 s2, and the byte with the s1 level
 };
 
 template <int MODE, bool DQ>
-__device__ __forceinline__ void rb_load(RbTile& tl, const CacheView& cv, int64_t seq, int t0, int lane, float2 s1_ls) {
+__device__ __forceinline__ void rb_load(RbTile& tl, const CacheView& cv, int64_t seq, int t0, int lane) {
   const int g = lane >> 2, p = lane & 3;
   const int64_t base = seq * (int64_t)cv.capacity + t0;
   const int tok = (lane & 7) + 8 * ((lane >> 3) & 1);
-  tl.code = __ldcs(reinterpret_cast<const uint2*>(cv.codes + (base + tok) * NSUB + 8 * (lane >> 4)));
+  tl.code = ld_v2(cv.codes + (base + tok) * NSUB + 8 * (lane >> 4));
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int64_t t = base + g + 8 * i;
     if constexpr (MODE == NSN_MODE_2BIT)
-      tl.sign[i] = __ldcs(reinterpret_cast<const uint32_t*>(cv.signs + t * NSUB) + p);
+      tl.sign[i] = ld_u32(cv.signs + t * NSUB + 4 * p);
     if constexpr (DQ) {
-      const uint32_t two = cv.s1_levels[t >> 1];
-      tl.s1[i] = fmaf((float)((t & 1) ? two >> 4 : two & 15u), s1_ls.y, s1_ls.x);
-      tl.s2[i] = __half2float(reinterpret_cast<const __half*>(cv.norms)[t]);
+      tl.level[i] = ld_u8(cv.s1_levels + (t >> 1));
+      tl.norm[i] = ld_u16(reinterpret_cast<const __half*>(cv.norms) + t);
     } else {
-      const float2 n = __half22float2(cv.norms[t]);
-      tl.s1[i] = n.x;
-      tl.s2[i] = n.y;
+      tl.norm[i] = ld_u32(cv.norms + t);
     }
   }
 }
@@ -133,7 +130,7 @@ readback_kernel(CacheView cv, int start, int n_tokens, const float* __restrict__
       }
       const int tb = u0 + ((lo - u0) & ~15);
       RbTile next;
-      rb_load<MODE, DQ>(next, cv, seq, tb, lane, s1_ls);
+      rb_load<MODE, DQ>(next, cv, seq, tb, lane);
       // H o of the block: the mean row as every token of one tile (fp16 hi + lo parts when it
       // is read back from levels; an fp16 mean row is its own hi part)
       {
@@ -170,7 +167,7 @@ readback_kernel(CacheView cv, int start, int n_tokens, const float* __restrict__
       }
       for (int t0 = tb; t0 < qhi; t0 += 16) {
         const RbTile cur = next;
-        if (t0 + 16 < qhi) rb_load<MODE, DQ>(next, cv, seq, t0 + 16, lane, s1_ls);
+        if (t0 + 16 < qhi) rb_load<MODE, DQ>(next, cv, seq, t0 + 16, lane);
         float E[8][2][4];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
@@ -196,8 +193,10 @@ readback_kernel(CacheView cv, int start, int n_tokens, const float* __restrict__
         float as[2], bs[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          bs[i] = cur.s1[i] * RB_INV_SQRT_D;
-          as[i] = bs[i] * cur.s2[i];
+          float2 n = __half22float2(*reinterpret_cast<const __half2*>(&cur.norm[i]));
+          if constexpr (DQ) n = make_float2(fmaf((float)((cur.level[i] >> (4 * (g & 1))) & 15u), s1_ls.y, s1_ls.x), n.x);
+          bs[i] = n.x * RB_INV_SQRT_D;
+          as[i] = bs[i] * n.y;
         }
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
@@ -211,11 +210,21 @@ readback_kernel(CacheView cv, int start, int n_tokens, const float* __restrict__
         }
       }
     }
-    for (int t = max(lo, nq); t < hi; ++t) {  // window rows, as they are
-      const uint2 x = *reinterpret_cast<const uint2*>(cv.window + (seq * cv.window_len + (t - nq)) * (int64_t)D + 4 * lane);
-      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&x.x));
-      const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&x.y));
-      rb_store4<DT>(out, row0 + (int64_t)t * st + 4 * lane, a.x, a.y, c.x, c.y);
+    // window rows, as they are: four reads in flight
+#pragma unroll 1
+    for (int t0 = max(lo, nq); t0 < hi; t0 += 4) {
+      uint2 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t0 + i < hi)
+          x[i] = ld_v2(cv.window + (seq * cv.window_len + (t0 + i - nq)) * (int64_t)D + 4 * lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t0 + i < hi) {
+          const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&x[i].x));
+          const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&x[i].y));
+          rb_store4<DT>(out, row0 + (int64_t)(t0 + i) * st + 4 * lane, a.x, a.y, c.x, c.y);
+        }
     }
   }
 }

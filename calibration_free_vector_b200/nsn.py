@@ -292,11 +292,27 @@ def nsn_append_residual(k_cache: Cache, v_cache: Cache, k_new, v_new, cb_k, cb_v
 
 
 def _one_device(first, *others):
-    """The device of `first`, which the other tensors must share; the call is made with it current."""
+    """Index of the CUDA device of `first`, which the other tensors must share."""
+    device = first.device
+    if device.type != "cuda":
+        raise ValueError(f"expected tensors on a CUDA device, got {device}")
     for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
-    return first.device
+        if t.device != device:
+            raise ValueError(f"tensors on different devices: {device} and {t.device}")
+    return device.index
+
+
+def _call_on(device: int, stream, fn, where: str, *args) -> None:
+    """Calls fn(*args, stream) with `device` current (the launches go to it), on `stream` or that
+    device's current stream."""
+    import torch
+    if torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            return _call_on(device, stream, fn, where, *args)
+    ptr = torch._C._cuda_getCurrentRawStream(device) if stream is None else int(stream.cuda_stream)
+    st = fn(*args, ptr)
+    if st != 0:
+        raise NsnError(st, where)
 
 
 def _check_codebook(*codebooks) -> None:
@@ -318,12 +334,9 @@ def nsn_dequantize_kv(cache: Cache, out, codebook, start: int = 0, stream=None) 
     if start < 0:
         raise ValueError("start must not be negative")
     _check_codebook(codebook)
-    import torch
-    with torch.cuda.device(_one_device(cache.codes, out, codebook)):
-        st = load().nsn_dequantize_kv(ctypes.byref(cache.c), start, out.shape[1], codebook.data_ptr(), out.data_ptr(),
-                                      _dtype_code(out), out.stride(0), out.stride(1), out.stride(2),
-                                      _stream_ptr(stream))
-    _check(st, "nsn_dequantize_kv")
+    sb, st, sh, _ = out.stride()
+    _call_on(_one_device(cache.codes, out, codebook), stream, load().nsn_dequantize_kv, "nsn_dequantize_kv",
+             ctypes.byref(cache.c), start, out.shape[1], codebook.data_ptr(), out.data_ptr(), _dtype_code(out), sb, st, sh)
 
 
 def nsn_selftest_bounded_wait(status, max_attempts: int = 8, stream=None) -> None:
@@ -405,7 +418,7 @@ def prefix_workspace(prefix_k: Cache, k_cache: Cache, n_q_heads: int, n_queries:
 def _check_prefix_call(prefix_k, prefix_v, k_cache, v_cache, q, cb_k, cb_v, out, workspace):
     if q.shape[-1] != HEAD_DIM or q.stride(-1) != 1 or q.shape[0] != k_cache.batch:
         raise ValueError("q must be [B, ..., H_q, 128] with the batch of the caches and a contiguous last dimension")
-    if not out.is_contiguous() or tuple(out.shape) != tuple(q.shape):
+    if not out.is_contiguous() or out.shape != q.shape:
         raise ValueError("out must be a contiguous tensor shaped like q")
     if not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous")
@@ -419,15 +432,12 @@ def nsn_decode_attention_prefix(prefix_k: Cache, prefix_v: Cache, k_cache: Cache
     prefix that the batch shares (caches of batch 1) and each sequence's own caches."""
     if q.dim() != 3:
         raise ValueError("q must be [B, H_q, 128]")
-    import torch
     device = _check_prefix_call(prefix_k, prefix_v, k_cache, v_cache, q, cb_k, cb_v, out, workspace)
-    with torch.cuda.device(device):
-        st = load().nsn_decode_attention_prefix(
-            ctypes.byref(prefix_k.c), ctypes.byref(prefix_v.c), ctypes.byref(k_cache.c), ctypes.byref(v_cache.c),
-            q.data_ptr(), _dtype_code(q), q.shape[1], q.stride(0), q.stride(1), float(softmax_scale), cb_k.data_ptr(),
-            cb_v.data_ptr(), out.data_ptr(), _dtype_code(out), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream_ptr(stream))
-    _check(st, "nsn_decode_attention_prefix")
+    sb, sh, _ = q.stride()
+    _call_on(device, stream, load().nsn_decode_attention_prefix, "nsn_decode_attention_prefix",
+             ctypes.byref(prefix_k.c), ctypes.byref(prefix_v.c), ctypes.byref(k_cache.c), ctypes.byref(v_cache.c),
+             q.data_ptr(), _dtype_code(q), q.shape[1], sb, sh, softmax_scale, cb_k.data_ptr(), cb_v.data_ptr(),
+             out.data_ptr(), _dtype_code(out), workspace.data_ptr(), workspace.nbytes)
 
 
 def nsn_extend_attention_prefix(prefix_k: Cache, prefix_v: Cache, k_cache: Cache, v_cache: Cache, q,
@@ -437,15 +447,12 @@ def nsn_extend_attention_prefix(prefix_k: Cache, prefix_v: Cache, k_cache: Cache
     quantized tokens and the own window up to its own token."""
     if q.dim() != 4:
         raise ValueError("q must be [B, C, H_q, 128]")
-    import torch
     device = _check_prefix_call(prefix_k, prefix_v, k_cache, v_cache, q, cb_k, cb_v, out, workspace)
-    with torch.cuda.device(device):
-        st = load().nsn_extend_attention_prefix(
-            ctypes.byref(prefix_k.c), ctypes.byref(prefix_v.c), ctypes.byref(k_cache.c), ctypes.byref(v_cache.c),
-            q.data_ptr(), _dtype_code(q), q.shape[2], q.shape[1], q.stride(0), q.stride(1), q.stride(2),
-            float(softmax_scale), cb_k.data_ptr(), cb_v.data_ptr(), out.data_ptr(), _dtype_code(out),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_ptr(stream))
-    _check(st, "nsn_extend_attention_prefix")
+    sb, st, sh, _ = q.stride()
+    _call_on(device, stream, load().nsn_extend_attention_prefix, "nsn_extend_attention_prefix",
+             ctypes.byref(prefix_k.c), ctypes.byref(prefix_v.c), ctypes.byref(k_cache.c), ctypes.byref(v_cache.c),
+             q.data_ptr(), _dtype_code(q), q.shape[2], q.shape[1], sb, st, sh, softmax_scale, cb_k.data_ptr(),
+             cb_v.data_ptr(), out.data_ptr(), _dtype_code(out), workspace.data_ptr(), workspace.nbytes)
 
 
 def nsn_decode_rope_workspace_bytes(k_cache: Cache, n_q_heads: int) -> int:
