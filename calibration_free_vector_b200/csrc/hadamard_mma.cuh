@@ -40,8 +40,16 @@ __device__ __forceinline__ void h16_mma(float (&d)[4], const uint32_t (&a)[4], c
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-// The H8 factor: butterflies over r.
+// The H8 factor: butterflies over r, two columns per instruction.
 __device__ __forceinline__ void h8_butterflies(float (&E)[8][2][4]) {
+  uint64_t e[8][2][2];
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) e[r][nt][i] = pack_f2(E[r][nt][2 * i], E[r][nt][2 * i + 1]);
+  const uint64_t minus = pack_f2(-1.f, -1.f);
 #pragma unroll
   for (int step = 1; step < 8; step <<= 1)
 #pragma unroll
@@ -50,11 +58,17 @@ __device__ __forceinline__ void h8_butterflies(float (&E)[8][2][4]) {
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float u = E[a][nt][i], w = E[a + step][nt][i];
-            E[a][nt][i] = u + w;
-            E[a + step][nt][i] = u - w;
+          for (int i = 0; i < 2; ++i) {
+            const uint64_t u = e[a][nt][i], w = e[a + step][nt][i];
+            e[a][nt][i] = add_f2(u, w);
+            e[a + step][nt][i] = fma_f2(w, minus, u);  // u - w (the product is exact)
           }
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) unpack_f2(e[r][nt][i], E[r][nt][2 * i], E[r][nt][2 * i + 1]);
 }
 
 }  // namespace nsn

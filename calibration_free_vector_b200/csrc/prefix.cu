@@ -260,23 +260,6 @@ __device__ __forceinline__ float ex2(float x) {
 // result is): the MMA operands derived from it then stay in uniform registers.
 __device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
 
-// Two fp32 values in a register pair, and arithmetic on both at once.
-__device__ __forceinline__ uint64_t pack_f2(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ void unpack_f2(uint64_t v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
-__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -905,6 +888,7 @@ __device__ __forceinline__ bool softmax_role(const PfArgs& a, PfSmem& sm, Cursor
     const int first = p.dual ? (group + pieces) & 1 : 0;
     const bool some = first < p.m;  // else nothing here waits for the MMAs, and no barrier may move
     if (some && wq == 0 && lane == 0) {
+      if (copies == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
       // (the group's MMAs that read the previous operand have finished: pv_done was waited for)
       const RowSet& r = p.own ? a.ro : a.rp;
       const unsigned char* src = q_tile(a, p.own, p.item, p.dual ? 0 : group);
@@ -1000,6 +984,7 @@ __device__ __forceinline__ bool softmax_role(const PfArgs& a, PfSmem& sm, Cursor
     tg0 += p.m;
     ++pieces;
   }
+  if (copies == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // (a group without tiles)
   return true;
 }
 
@@ -1072,12 +1057,15 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_kernel(const __grid_cons
     total += sm.scan[w];
   }
   // at least one unit each, so the CTAs with tiles of an item are consecutive
-  // (nothing above depends on the kernel before this one in the stream; the join, which does, may
-  // be scheduled from here on and waits for this kernel's end)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The counters and caches were there before the whole call; of the kernels before this one only the
+  // query tiles are needed, and whoever copies one waits (griddepcontrol.wait) first.  The join may be
+  // scheduled from here on and waits for this kernel's end.
   asm volatile("griddepcontrol.launch_dependents;");
   const long long ctas = min((long long)gridDim.x, total), bid = blockIdx.x;
-  if (bid >= ctas) return;  // the whole CTA: nothing to do
+  if (bid >= ctas) {  // the whole CTA: nothing to do (the kernels before this one still end first)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const long long begin = total * bid / ctas, end = total * (bid + 1) / ctas;
   long long at = before + inc - sum;  // tiles before this thread's segments
   if (at <= begin && begin < at + sum) {
@@ -1147,10 +1135,9 @@ constexpr int JOIN_DEPTH = 8;  // partials read at once
 
 // Partials wi, wi + WPR, ... of one item, added to (m, l, v).
 template <int WPR>
-__device__ __forceinline__ void join_item(const PfArgs& a, bool own, int seg, int row, int wi, int lane, float& m, float& l, float (&v)[4]) {
+__device__ __forceinline__ void join_item(const PfArgs& a, bool own, int seg, int tiles, int row, int wi, int lane, float& m, float& l, float (&v)[4]) {
   const RowSet& r = own ? a.ro : a.rp;
   const int64_t item = (int64_t)(own ? seg - a.H : seg) * r.rt + row / 256;
-  const int tiles = seg_info(a, seg).tiles;
   const int2 ctas = a.tab[(own ? (int64_t)a.H * a.rp.rt : 0) + item];
   if (tiles == 0) return;  // (then the table says nothing)
   const int in = row % 256;
@@ -1202,7 +1189,6 @@ template <int WPR>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) prefix_join_kernel(const __grid_constant__ PfArgs a, void* __restrict__ out, int odt) {
   __shared__ float4 sv[JOIN_WARPS][32];
   __shared__ float2 sml[JOIN_WARPS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wi = warp % WPR;
   const int64_t r = ((int64_t)blockIdx.x * JOIN_WARPS + warp) / WPR;  // (b, c, head)
   const int nh = a.H * a.G;
@@ -1210,14 +1196,20 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) prefix_join_kernel(const __gr
   float2 own = make_float2(NEG_BIG, 0.f);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = NEG_BIG, l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+  const int hq = (int)(r % nh), bc = (int)(r / nh), c = bc % a.C, b = bc / a.C, h = hq / a.G, gi = hq % a.G;
+  int tiles_p = 0, tiles_o = 0;
+  if (live) {  // (the counters were there before the whole call)
+    tiles_p = seg_info(a, h).tiles;
+    tiles_o = a.own_lse ? 0 : seg_info(a, a.H + b * a.H + h).tiles;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (live) {
     if (a.own_lse && wi == 0) {
       own = a.own_lse[r];
       o = *reinterpret_cast<const float4*>(a.own_out + r * D + 4 * lane);
     }
-    const int hq = (int)(r % nh), bc = (int)(r / nh), c = bc % a.C, b = bc / a.C, h = hq / a.G, gi = hq % a.G;
-    join_item<WPR>(a, false, h, (b * a.C + c) * a.G + gi, wi, lane, m, l, v);
-    if (!a.own_lse) join_item<WPR>(a, true, a.H + b * a.H + h, c * a.G + gi, wi, lane, m, l, v);
+    join_item<WPR>(a, false, h, tiles_p, (b * a.C + c) * a.G + gi, wi, lane, m, l, v);
+    if (!a.own_lse) join_item<WPR>(a, true, a.H + b * a.H + h, tiles_o, c * a.G + gi, wi, lane, m, l, v);
   }
   if constexpr (WPR > 1) {  // the row's first warp adds the others' sums
     sv[warp][lane] = make_float4(v[0], v[1], v[2], v[3]);

@@ -2,14 +2,15 @@
 // ordinary row of fp32, bf16 or fp16.
 //
 // For a quantized token t of block b, with H the orthonormal Hadamard matrix,
-//   x_hat = H ((u_hat s2 + o_b) s1) = (s1 s2) (H u_hat) + s1 (H o_b)        (H^T = H),
+//   x_hat = H ((u_hat s2 + o_b) s1) = ((H u_hat) s2 + H o_b) s1        (H^T = H),
 // so H is applied to the codewords themselves, which are exact in fp16, and the norms
 // enter in fp32 afterwards; H o_b is formed once per unit of work.
 //
 // The transform is the one of hadamard_mma.cuh (M = the 16 tokens of a tile).  Its A operand,
 // for each r the 16 values of sub-vectors 2r and 2r + 1, is gathered by ldmatrix straight from an
 // 8-fold replicated fp16 codebook, the stored signs XOR-ed on.  A lane ends with four consecutive
-// dims of a row: 8- or 16-byte stores, every 32-byte sector written whole.
+// dims of a row: 8- or 16-byte stores, every 32-byte sector written whole (rows sent through shared
+// memory with one bulk copy each were no faster: 275 against 266 us for 16 x 8 x 32768 bf16 rows).
 
 #include "hadamard_mma.cuh"
 #include "nsn_launch.h"
@@ -109,8 +110,11 @@ readback_kernel(CacheView cv, int start, int n_tokens, const float* __restrict__
   const int unit_tok = 16 * unit_tiles;
   const int first_unit = start / unit_tok;
   for (int64_t unit = (int64_t)blockIdx.x * RB_WARPS + warp; unit < n_units; unit += (int64_t)gridDim.x * RB_WARPS) {
-    const int64_t seq = unit / units_per_seq;
-    const int u0 = (first_unit + (int)(unit % units_per_seq)) * unit_tok;  // first token of the unit
+    // the heads of one token range are consecutive units: with rows [B, T, H, 128] they write one
+    // contiguous stretch of memory at about the same time
+    const int64_t bu = unit / cv.n_kv_heads;
+    const int64_t seq = bu / units_per_seq * cv.n_kv_heads + unit % cv.n_kv_heads;
+    const int u0 = (first_unit + (int)(bu % units_per_seq)) * unit_tok;  // first token of the unit
     const int nq = max(0, min(cv.n_quant[seq], cv.capacity));
     const int nw = cv.window_len > 0 ? max(0, min(cv.n_window[seq], cv.window_len)) : 0;
     const int lo = max(u0, start), hi = min(u0 + unit_tok, min(start + n_tokens, nq + nw));
@@ -190,23 +194,26 @@ readback_kernel(CacheView cv, int start, int n_tokens, const float* __restrict__
         const int t = t0 + g;
         const bool have[2] = {t >= lo && t < qhi, t + 8 >= lo && t + 8 < qhi};
         const int64_t off = row0 + (int64_t)t * st + 4 * p;
-        float as[2], bs[2];
+        uint64_t s1[2], s2[2];  // s1 / sqrt(128) and s2 of the two tokens, for two columns at once
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float2 n = __half22float2(*reinterpret_cast<const __half2*>(&cur.norm[i]));
           if constexpr (DQ) n = make_float2(fmaf((float)((cur.level[i] >> (4 * (g & 1))) & 15u), s1_ls.y, s1_ls.x), n.x);
-          bs[i] = n.x * RB_INV_SQRT_D;
-          as[i] = bs[i] * n.y;
+          s1[i] = pack_f2(n.x * RB_INV_SQRT_D, n.x * RB_INV_SQRT_D);
+          s2[i] = pack_f2(n.y, n.y);
         }
+        const uint64_t zero = pack_f2(0.f, 0.f);
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
           const float4 ho = *reinterpret_cast<const float4*>(&sm.ho[warp][16 * r + 4 * p]);
+          const uint64_t h01 = pack_f2(ho.x, ho.y), h23 = pack_f2(ho.z, ho.w);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (have[i])
-              rb_store4<DT>(out, off + 8 * i * st + 16 * r, fmaf(as[i], E[r][0][2 * i], bs[i] * ho.x),
-                            fmaf(as[i], E[r][0][2 * i + 1], bs[i] * ho.y), fmaf(as[i], E[r][1][2 * i], bs[i] * ho.z),
-                            fmaf(as[i], E[r][1][2 * i + 1], bs[i] * ho.w));
+          for (int i = 0; i < 2; ++i) {
+            float v[4];  // ((H u_hat) s2 + H o) s1
+            unpack_f2(fma_f2(fma_f2(pack_f2(E[r][0][2 * i], E[r][0][2 * i + 1]), s2[i], h01), s1[i], zero), v[0], v[1]);
+            unpack_f2(fma_f2(fma_f2(pack_f2(E[r][1][2 * i], E[r][1][2 * i + 1]), s2[i], h23), s1[i], zero), v[2], v[3]);
+            if (have[i]) rb_store4<DT>(out, off + 8 * i * st + 16 * r, v[0], v[1], v[2], v[3]);
+          }
         }
       }
     }
@@ -238,12 +245,13 @@ cudaError_t launch_t(const CacheView& cv, int start, int n_tokens, const float* 
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int64_t nseq = (int64_t)cv.batch * cv.n_kv_heads, ctas = (int64_t)sms * RB_CTAS;
-  // A whole block per unit forms H o once per 128 tokens; with fewer blocks than warps the
-  // units are made smaller so that every warp has one.
+  // A whole block per unit forms H o once per 128 tokens; units are made smaller until every resident
+  // warp has four, so that ragged lengths even out (128 ragged sequences of up to 4002 tokens: 31 us,
+  // with one unit per warp 39; 8 sequences of 4096, host-bound either way).
   int unit_tiles = BLK / 16;
   const int64_t end = (int64_t)start + n_tokens;
   const auto per_seq = [&](int tiles) { return (end + 16 * tiles - 1) / (16 * tiles) - start / (16 * tiles); };
-  while (unit_tiles > 1 && nseq * per_seq(unit_tiles) < ctas * RB_WARPS) unit_tiles >>= 1;
+  while (unit_tiles > 1 && nseq * per_seq(unit_tiles) < 4 * ctas * RB_WARPS) unit_tiles >>= 1;
   const int64_t ups = per_seq(unit_tiles), n_units = nseq * ups;
   const int64_t want = (n_units + RB_WARPS - 1) / RB_WARPS;
   readback_kernel<MODE, DQ, DT><<<(unsigned)(want < ctas ? want : ctas), 32 * RB_WARPS, sizeof(RbSmem), s>>>(
