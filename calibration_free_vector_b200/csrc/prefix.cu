@@ -45,7 +45,7 @@ constexpr int PF_THREADS = 32 * (8 + PF_DEQ_WARPS + 4);  // the last warpgroup: 
 // the warps may not pass 20 x 96 = 1920: 8 x 104 + 8 x 120 + 4 x 32.
 constexpr int PF_REGS_SOFTMAX = 104, PF_REGS_DECODE = 120, PF_REGS_MMA = 32;
 static_assert(8 * PF_REGS_SOFTMAX + PF_DEQ_WARPS * PF_REGS_DECODE + 4 * PF_REGS_MMA <= (PF_THREADS / 32) * 96, "registers of the CTA");
-constexpr int PF_RING = 4;         // K / V tiles in shared memory
+constexpr int PF_BUFS = 2;         // buffers of K tiles, and of V tiles, in shared memory (tile g of the CTA in buffer g & 1)
 constexpr int PF_REP = 4;          // replicas of each codeword
 constexpr int PF_TILE_BYTES = 32768;  // 128 tokens (or rows) x 128 dims fp16: two 16 KB halves of 64 dims
 constexpr uint32_t PF_HALF = 16384u;
@@ -93,14 +93,14 @@ struct PfInfo {            // of one tile, for the softmax
 
 struct PfSmem {
   alignas(1024) unsigned char q[2][PF_TILE_BYTES];
-  alignas(1024) unsigned char ring[PF_RING][PF_TILE_BYTES];
+  alignas(1024) unsigned char kv[2][PF_BUFS][PF_TILE_BYTES];  // K tiles, V tiles
   alignas(128) uint4 cbk[NCODES][PF_REP];
   alignas(128) uint4 cbv[NCODES][PF_REP];
   alignas(16) unsigned char o[PF_DEQ_WARPS][256];  // the mean row of the tile a decode warp is at
   alignas(16) PfInfo info[4];
   float red[2][2][2][PF_TEAM];     // per team (double-buffered: window tiles in turn): K and V scales
   int red_bad[2][2][PF_TEAM];
-  alignas(8) uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], full[PF_RING], empty[PF_RING], meet[2], drain[2];
+  alignas(8) uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], full[2][PF_BUFS], empty[2][PF_BUFS], meet[2], drain[2];
   long long scan[PF_THREADS / 32];
   long long units;
   int seg0, rt0, u0;
@@ -328,10 +328,6 @@ __device__ __forceinline__ bool next_piece(const PfArgs& a, Cursor& c, Piece& p)
   } while (p.m == 0);  // (the range ended inside the item's overhead)
   return true;
 }
-// Ring index, from the piece's base, of tile t's K and V: the order is K0 K1 V0 K2 V1 ... V(m-1).
-__device__ __forceinline__ int ring_k(int t) { return t == 0 ? 0 : 2 * t - 1; }
-__device__ __forceinline__ int ring_v(int t, int m) { return t + 1 < m ? 2 * t + 2 : 2 * m - 1; }
-
 // Partial slots: a CTA walks the items in order, so (item + CTA) names each (item, CTA) pair
 // once; prefix items' slots come first.
 __device__ __forceinline__ int64_t slot_row(const PfArgs& a, bool own, int64_t item, int64_t cta) {
@@ -453,22 +449,38 @@ __device__ __forceinline__ void tile_write(const Raw& r, const uint4 (*cb)[PF_RE
   const bool live = row < nvalid;
   const uint4* rep = &cb[0][lane & (PF_REP - 1)];
   const uint32_t sw[4] = {r.sign.x, r.sign.y, r.sign.z, r.sign.w};
+  // Four sub-vectors at a time, the next four's reads before this four's writes: the compiler keeps
+  // reads behind writes that might alias them, and each would wait out the latency of the one before.
+  uint4 c[2][4], o[2][4];
+  const auto gather = [&](int s0, uint4 (&cw)[4], uint4 (&om)[4]) {
 #pragma unroll
-  for (int s = 0; s < NSUB; ++s) {  // the record holds the even sub-vectors' codes, then the odd ones'
-    const uint32_t word = (s & 1) ? ((s >> 1) < 4 ? r.code.z : r.code.w) : ((s >> 1) < 4 ? r.code.x : r.code.y);
-    const uint32_t code = __byte_perm(word, 0u, 0x4440u | (uint32_t)((s >> 1) & 3));
-    const uint4 c = rep[code * PF_REP];
-    const uint4 o = *reinterpret_cast<const uint4*>(orow + 16 * s);
-    uint32_t u[4] = {c.x, c.y, c.z, c.w};
-    const uint32_t om[4] = {o.x, o.y, o.z, o.w};
-    if constexpr (MODE == NSN_MODE_2BIT) {  // the sign of dim 8 s + i is bit 15 - s of field i
-#pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] ^= (sw[i] << s) & 0x80008000u;
+    for (int i = 0; i < 4; ++i) {  // the record holds the even sub-vectors' codes, then the odd ones'
+      const int s = s0 + i;
+      const uint32_t word = (s & 1) ? ((s >> 1) < 4 ? r.code.z : r.code.w) : ((s >> 1) < 4 ? r.code.x : r.code.y);
+      const uint32_t code = __byte_perm(word, 0u, 0x4440u | (uint32_t)((s >> 1) & 3));
+      cw[i] = rep[code * PF_REP];
+      om[i] = *reinterpret_cast<const uint4*>(orow + 16 * s);
     }
+  };
+  gather(0, c[0], o[0]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = as_u32(__hfma2(as_h2(u[i]), a2, __hmul2(as_h2(om[i]), b2)));
-    *reinterpret_cast<uint4*>(dst + (s >> 3) * PF_HALF + (((s & 7) ^ (row & 7)) << 4)) =
-        live ? make_uint4(u[0], u[1], u[2], u[3]) : make_uint4(0u, 0u, 0u, 0u);
+  for (int s0 = 0; s0 < NSUB; s0 += 4) {
+    const int now = (s0 >> 2) & 1;
+    if (s0 + 4 < NSUB) gather(s0 + 4, c[now ^ 1], o[now ^ 1]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int s = s0 + j;
+      uint32_t u[4] = {c[now][j].x, c[now][j].y, c[now][j].z, c[now][j].w};
+      const uint32_t om[4] = {o[now][j].x, o[now][j].y, o[now][j].z, o[now][j].w};
+      if constexpr (MODE == NSN_MODE_2BIT) {  // the sign of dim 8 s + i is bit 15 - s of field i
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] ^= (sw[i] << s) & 0x80008000u;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = as_u32(__hfma2(as_h2(u[i]), a2, __hmul2(as_h2(om[i]), b2)));
+      *reinterpret_cast<uint4*>(dst + (s >> 3) * PF_HALF + (((s & 7) ^ (row & 7)) << 4)) =
+          live ? make_uint4(u[0], u[1], u[2], u[3]) : make_uint4(0u, 0u, 0u, 0u);
+    }
   }
 }
 
@@ -577,9 +589,9 @@ __device__ __forceinline__ bool decode_role(const PfArgs& a, PfSmem& sm, Cursor 
       const uint4 c4 = v4;
       const uint2 cp = vp;
       if (t + 1 < p.m) fetch(t + 1);
-      const int n = 2 * tg0 + (TV ? ring_v(t, p.m) : ring_k(t)), slot = n % PF_RING, blk = p.j + t;
-      if (n >= PF_RING && !bar_wait(&sm.empty[slot], (uint32_t)(n / PF_RING - 1), &sm.fail)) return false;
-      unsigned char* tile = sm.ring[slot];
+      const int g = tg0 + t, buf = g & 1, blk = p.j + t;
+      if (g >= PF_BUFS && !bar_wait(&sm.empty[TV][buf], (uint32_t)(g / PF_BUFS - 1), &sm.fail)) return false;
+      unsigned char* tile = sm.kv[TV][buf];
       PfInfo info;
       if (blk < p.s.blocks) {
         const int nvalid = min(BLK, p.s.nq - BLK * blk);
@@ -598,7 +610,7 @@ __device__ __forceinline__ bool decode_role(const PfArgs& a, PfSmem& sm, Cursor 
         float smax = 0.f, vmax = 0.f;
         int vbad = BLK;
         uint32_t f[8][4];
-        const uint32_t buf = met & 1;
+        const uint32_t side = met & 1;
 #pragma unroll 1
         for (int i = 0; i < (TV ? 2 : 4); ++i) {
           float mine;
@@ -614,16 +626,16 @@ __device__ __forceinline__ bool decode_role(const PfArgs& a, PfSmem& sm, Cursor 
           }
         }
         if (lane == 0) {
-          sm.red[TV][buf][0][w] = smax;
-          sm.red[TV][buf][1][w] = vmax;
-          sm.red_bad[TV][buf][w] = vbad;
+          sm.red[TV][side][0][w] = smax;
+          sm.red[TV][side][1][w] = vmax;
+          sm.red_bad[TV][side][w] = vbad;
         }
         if (!decode_sync(sm, TV, met, lane)) return false;
 #pragma unroll
         for (int x = 0; x < PF_TEAM; ++x) {
-          smax = fmaxf(smax, sm.red[TV][buf][0][x]);
-          vmax = fmaxf(vmax, sm.red[TV][buf][1][x]);
-          vbad = min(vbad, sm.red_bad[TV][buf][x]);
+          smax = fmaxf(smax, sm.red[TV][side][0][x]);
+          vmax = fmaxf(vmax, sm.red[TV][side][1][x]);
+          vbad = min(vbad, sm.red_bad[TV][side][x]);
         }
 #pragma unroll 1
         for (int i = 1; i >= 0; --i) {  // (the second 16 rows are still in f)
@@ -640,11 +652,11 @@ __device__ __forceinline__ bool decode_role(const PfArgs& a, PfSmem& sm, Cursor 
       if (!TV && w == 0 && lane == 0) {
         info.lv = log2f(info.iva);
         info.iva = 1.f / info.iva;
-        sm.info[(tg0 + t) & 3] = info;
+        sm.info[g & 3] = info;
       }
       fence_async();
       __syncwarp();
-      if (lane == 0) bar_arrive(&sm.full[slot]);
+      if (lane == 0) bar_arrive(&sm.full[TV][buf]);
     }
     tg0 += p.m;
   }
@@ -655,10 +667,12 @@ __device__ __forceinline__ bool decode_role(const PfArgs& a, PfSmem& sm, Cursor 
 // The MMA warps, one per softmax group (one warp for both spent longer issuing than the products
 // took).  S and P of a group are two halves of 64 tokens: while the softmax works on one, the products
 // of the other run, so its scores are there when it is done.  S = Q K^T of a half needs the K tile and
-// its previous P consumed, O += P V the V tile and P.  Each warp walks every tile of every piece in ring
-// order and frees it, by a commit behind its own products or, where the other group alone uses
-// the tile, at once: no tile is replaced before both have seen it, so a barrier's parity is never
-// ambiguous.  The warps stay converged (votes decide).
+// its previous P consumed, O += P V the V tile and P.  Each warp walks every tile of every piece in
+// order and frees it, by a commit behind its own products or, where the other group alone uses the
+// tile, at once.  No tile is replaced before both warps have seen it, K tiles and V tiles have
+// buffers and barriers of their own, each filled by one team in order: so whoever waits has seen the
+// phase before the one it waits for, and a barrier's parity is never ambiguous.  The warps stay
+// converged (votes decide).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ bool test_all(uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, bar_test(b, parity)); }
 
@@ -667,51 +681,49 @@ __device__ __forceinline__ bool mma_role(const PfArgs& a, PfSmem& sm, Cursor cur
   // descriptors differ from these only by constant steps of the start address (16-byte units)
   const uint32_t tmem = (uint32_t)uniform((int)sm.tmem);
   const uint32_t s_col = tmem + 128u * group, o_col = tmem + 256u + 128u * group;
-  const uint32_t q_lo = desc_lo(sm_addr(sm.q[0]), 16u) + TILE * group, k_lo = desc_lo(sm_addr(sm.ring[0]), 16u),
-                 v_lo = desc_lo(sm_addr(sm.ring[0]), PF_HALF);
+  const uint32_t q_lo = desc_lo(sm_addr(sm.q[0]), 16u) + TILE * group, k_lo = desc_lo(sm_addr(sm.kv[0][0]), 16u),
+                 v_lo = desc_lo(sm_addr(sm.kv[1][0]), PF_HALF);
   uint64_t *s_full = sm.s_full[group], *p_full = sm.p_full[group], *pv_done = sm.pv_done[group];
   Piece p;
-  int n0 = 0, pieces = 0, seen = 0;        // ring index of the piece, pieces before it, ring tiles seen
-  uint32_t slot_seen = 0u, parity = 0u;    // of the next ring tile
+  int g0 = 0, pieces = 0;                  // tiles and pieces before this piece
+  int seen[2] = {0, 0};                    // K and V tiles seen, over all pieces
   uint32_t done = 0u, built = 0u;          // tiles finished and query operands used, over all pieces
   uint32_t idle = 0;
   while (next_piece(a, cur, p)) {
     const int m = uniform(p.m), step = uniform(p.dual ? 2 : 1), first = step == 2 ? (group + pieces) & 1 : 0;
-    const int halves = first < m ? 2 * ((m - first + step - 1) / step) : 0, end = n0 + 2 * m;
+    const int halves = first < m ? 2 * ((m - first + step - 1) / step) : 0, end = g0 + m;
     int qk = 0, pv = 0;                    // next half tile of each product
     bool have_q = false;
-    while (pv < halves || seen < end) {
+    while (pv < halves || seen[0] < end || seen[1] < end) {
       bool moved = false;
-      if (seen < end && test_all(&sm.full[slot_seen], parity)) {
-        const int r = seen - n0;           // K0 K1 V0 K2 V1 ... V(m-1)
-        const int t = r == 0 ? 0 : r == 2 * m - 1 ? m - 1 : (r & 1) ? (r + 1) >> 1 : (r >> 1) - 1;
-        if (step == 2 && ((t - first) & 1) && (threadIdx.x & 31) == 0) bar_arrive(&sm.empty[slot_seen]);
-        ++seen;
-        if (++slot_seen == PF_RING) {
-          slot_seen = 0u;
-          parity ^= 1u;
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const int g = seen[v], buf = g & 1;
+        if (g < end && test_all(&sm.full[v][buf], (uint32_t)(g / PF_BUFS))) {
+          if (step == 2 && ((g - g0 - first) & 1) && (threadIdx.x & 31) == 0) bar_arrive(&sm.empty[v][buf]);
+          ++seen[v];
+          moved = true;
         }
-        moved = true;
       }
       if (pv < qk) {  // O += P V of half pv
-        const int t = first + step * (pv >> 1), h = pv & 1, n = n0 + ring_v(t, m), slot = n % PF_RING;
-        if (n < seen && test_all(&p_full[h], done + (uint32_t)(pv >> 1))) {
+        const int t = first + step * (pv >> 1), h = pv & 1, g = g0 + t, buf = g & 1;
+        if (g < seen[1] && test_all(&p_full[h], done + (uint32_t)(pv >> 1))) {
           tc_after();
-          mma_pv(o_col, s_col + 64u * h, v_lo + TILE * (uint32_t)slot + 512u * h, pv > 0);
+          mma_pv(o_col, s_col + 64u * h, v_lo + TILE * (uint32_t)buf + 512u * h, pv > 0);
           tc_commit_to(&pv_done[h]);
-          if (h) tc_commit_to(&sm.empty[slot]);
+          if (h) tc_commit_to(&sm.empty[1][buf]);
           ++pv;
           moved = true;
         }
       }
       if (qk < halves && qk < pv + 2) {  // S = Q K^T of half qk, two ahead of O at most
-        const int t = first + step * (qk >> 1), h = qk & 1, n = n0 + ring_k(t), slot = n % PF_RING;
+        const int t = first + step * (qk >> 1), h = qk & 1, g = g0 + t, buf = g & 1;
         if (!have_q) have_q = test_all(&sm.q_full[group], built);
-        if (have_q && n < seen && (qk < 2 || test_all(&pv_done[h], done + (uint32_t)(qk >> 1) - 1u))) {
+        if (have_q && g < seen[0] && (qk < 2 || test_all(&pv_done[h], done + (uint32_t)(qk >> 1) - 1u))) {
           tc_after();
-          mma_qk(s_col + 64u * h, q_lo, k_lo + TILE * (uint32_t)slot + 512u * h);
+          mma_qk(s_col + 64u * h, q_lo, k_lo + TILE * (uint32_t)buf + 512u * h);
           tc_commit_to(&s_full[h]);
-          if (h) tc_commit_to(&sm.empty[slot]);
+          if (h) tc_commit_to(&sm.empty[0][buf]);
           ++qk;
           moved = true;
         }
@@ -721,7 +733,7 @@ __device__ __forceinline__ bool mma_role(const PfArgs& a, PfSmem& sm, Cursor cur
     }
     done += (uint32_t)(halves >> 1);
     built += halves ? 1u : 0u;
-    n0 = end;
+    g0 = end;
     ++pieces;
   }
   return true;
@@ -1038,10 +1050,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_kernel(const __grid_cons
         bar_init(&sm.pv_done[i][h], 1);
       }
     }
-    for (int i = 0; i < PF_RING; ++i) {
-      bar_init(&sm.full[i], PF_TEAM);
-      bar_init(&sm.empty[i], 2);
-    }
+    for (int v = 0; v < 2; ++v)
+      for (int i = 0; i < PF_BUFS; ++i) {
+        bar_init(&sm.full[v][i], PF_TEAM);
+        bar_init(&sm.empty[v][i], 2);
+      }
     bar_init(&sm.meet[0], PF_TEAM);
     bar_init(&sm.meet[1], PF_TEAM);
     bar_init(&sm.drain[0], 1);
