@@ -210,8 +210,9 @@ nsn_status nsn_dequantize_kv(const nsn_cache* cache, int start, int n_tokens, co
   if (n_tokens == 0) return NSN_OK;
   if (!out || !aligned16(out)) return NSN_ERR_INVALID_ARG;
   if (!rows_apart(cache->batch, stride_b, n_tokens, stride_t, cache->n_kv_heads, stride_h)) return NSN_ERR_INVALID_ARG;
-  // no sequence has tokens past its buffers' end
-  const int64_t most = (int64_t)cache->capacity + cache->window - start;
+  // no sequence has tokens past its buffers' end (and positions stay inside 32 bits)
+  const int64_t end = (int64_t)cache->capacity + cache->window;
+  const int64_t most = (end < INT32_MAX - NSN_BLOCK ? end : INT32_MAX - NSN_BLOCK) - start;
   if (most <= 0) return NSN_OK;
   return cuda_status(nsn::launch_readback(view(cache), start, (int)(n_tokens < most ? n_tokens : most), codebook, out,
                                           dtype, stride_b, stride_t, stride_h, static_cast<cudaStream_t>(stream)));

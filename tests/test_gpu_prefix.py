@@ -276,3 +276,73 @@ def test_prefix_strided_queries_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     pt.check(*caches, q, out, cbk, cbv, 2, 2, SCALE)
+
+
+def test_prefix_without_any_token():
+    caches = make([(0, 0)], [[(0, 0)], [(0, 0)]], 2, 2, False, seed=81)
+    cbk, cbv, dk, dv = books(2, 2)
+    assert torch.all(decode(caches, queries((2, 4, 128), torch.bfloat16, 1), dk, dv) == 0)
+    assert torch.all(extend(caches, queries((2, 3, 4, 128), torch.bfloat16, 1), dk, dv, status=8) == 0)
+
+
+def test_prefix_calls_on_two_streams():
+    # two batches over one prefix at the same time, each with its own workspace
+    B, H, g, C = 24, 2, 4, 40
+    pk, pv, kc, vc = make([(5120, 100)] * H, own_counts(B, H), 2, 1, False, seed=83)
+    own = [[(128 * (b % 2), 40 + 7 * h) for h in range(H)] for b in range(3)]
+    _, _, kx, vx = make([(128, 0)] * H, own, 2, 1, False, seed=85)
+    cbk, cbv, dk, dv = books(2, 1)
+    q, qx = queries((B, H * g, 128), torch.bfloat16, 16), queries((3, C, H * g, 128), torch.float16, 17)
+    want, wantx = decode((pk, pv, kc, vc), q, dk, dv), extend((pk, pv, kx, vx), qx, dk, dv)
+    ws, wsx = workspace(pk, kc, H * g), workspace(pk, kx, H * g, C)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [(torch.empty_like(q), torch.empty_like(qx)) for _ in range(8)]
+    torch.cuda.synchronize()
+    for out, outx in outs:
+        nsn.nsn_decode_attention_prefix(pk, pv, kc, vc, q, SCALE, dk, dv, out, ws, stream=streams[0])
+        nsn.nsn_extend_attention_prefix(pk, pv, kx, vx, qx, SCALE, dk, dv, outx, wsx, stream=streams[1])
+    torch.cuda.synchronize()
+    for out, outx in outs:
+        assert torch.equal(out, want) and torch.equal(outx, wantx)
+    pt.check(pk, pv, kx, vx, qx, wantx, cbk, cbv, 2, 1, SCALE, chunk=C)
+
+
+def test_extend_prefix_past_32_bit_offsets():
+    # own caches whose later sequences start more than 4 GB into their buffers
+    cap, C, g = 1 << 27, 2, 4
+    small = make([(256, 0)] * 3, [[(256, 20), (128, 9), (384, 128)]], 1, 1, False, seed=87, poison=False)
+    big = []
+    for c in small[2:]:
+        d = nsn.Cache(1, 3, cap, 128, 1)
+        n = c.capacity
+        d.codes[:, :, :n], d.norms[:, :, :n], d.means[:, :, :n // 128] = c.codes, c.norms, c.means
+        d.window_buf.copy_(c.window_buf)
+        d.n_quant.copy_(c.n_quant)
+        d.n_window.copy_(c.n_window)
+        big.append(d)
+    cbk, cbv, dk, dv = books(1, 1)
+    q = queries((1, C, 3 * g, 128), torch.bfloat16, 18)
+    out = extend((*small[:2], *big), q, dk, dv)
+    pt.check(*small, q, out, cbk, cbv, 1, 1, SCALE, chunk=C)
+
+
+def test_prefix_refuses_what_it_cannot_take():
+    caches = make([(128, 3)], [[(128, 3)], [(0, 9)]], 2, 2, False, seed=89)
+    cbk, cbv, dk, dv = books(2, 2)
+    q, out = queries((2, 4, 128), torch.bfloat16, 1), torch.empty((2, 4, 128), device="cuda")
+    ws = workspace(caches[0], caches[2], 4)
+    good = dict(q=q, out=out, ws=ws, dk=dk)
+    for bad in (dict(q=q[:1], out=out[:1]), dict(q=q[0]), dict(q=q.cpu()), dict(out=out[:1]), dict(out=out.cpu()),
+                dict(out=torch.empty((4, 2, 128), device="cuda").transpose(0, 1)), dict(dk=dk.cpu()), dict(dk=dk.half()),
+                dict(q=q[..., :64]), dict(ws=ws[::2])):
+        a = good | bad
+        with pytest.raises(ValueError):
+            nsn.nsn_decode_attention_prefix(*caches, a["q"], SCALE, a["dk"], dv, a["out"], a["ws"])
+    for bad in (dict(ws=ws[:-256]), dict(ws=ws[16:])):
+        a = good | bad
+        with pytest.raises(nsn.NsnError):
+            nsn.nsn_decode_attention_prefix(*caches, a["q"], SCALE, a["dk"], dv, a["out"], a["ws"])
+    with pytest.raises(nsn.NsnError):     # the own caches' batch is not 1
+        nsn.nsn_decode_attention_prefix(caches[2], caches[3], *caches[2:], q, SCALE, dk, dv, out, ws)
+    with pytest.raises(ValueError):
+        nsn.prefix_workspace(caches[0], caches[2], 6)

@@ -135,3 +135,37 @@ def test_readback_of_what_the_quantizer_wrote():
     assert torch.equal(out[:, nq:], x[:, nq:].half().float())     # the window holds fp16
     cos = torch.nn.functional.cosine_similarity(out[:, :nq], x[:, :nq].float(), dim=-1)
     assert float(cos.min()) > 0.8
+
+
+def test_readback_past_32_bit_offsets():
+    # records more than 4 GB into the buffers: the last tokens of the last of three long sequences
+    cap, n = 1 << 27, 300
+    cache = nsn.Cache(1, 3, cap, 0, 1)
+    small = ct.random_cache([[(n, 0)]], 384, 0, 1, False, seed=77, poison=False)
+    off = cap - 384
+    cache.codes[0, 2, off:] = small.codes[0, 0]
+    cache.norms[0, 2, off:] = small.norms[0, 0]
+    cache.means[0, 2, off // 128:] = small.means[0, 0]
+    cache.n_quant[0, 2] = off + n
+    cb = tl.codebook(1)
+    out = torch.full((1, 384, 3, 128), SENTINEL, dtype=torch.float32, device="cuda")
+    nsn.nsn_dequantize_kv(cache, out, torch.from_numpy(cb).cuda(), start=off)
+    check(small, out[:, :, 2:], 0, cb, 1)
+    assert torch.all(out[:, :, :2] == SENTINEL)
+
+
+def test_readback_refuses_what_it_cannot_take():
+    cache = ct.random_cache([[(128, 3)]], 128, 128, 2, False, seed=1)
+    dcb = torch.from_numpy(tl.codebook(2)).cuda()
+    out = torch.empty((1, 131, 1, 128), dtype=torch.float32, device="cuda")
+    call = nsn.nsn_dequantize_kv
+    for bad in (dict(out=out[0]), dict(out=out[..., :64]), dict(out=torch.empty((2, 131, 1, 128), device="cuda")),
+                dict(out=out.cpu()), dict(codebook=dcb.cpu()), dict(codebook=dcb.half()), dict(codebook=dcb[:100]),
+                dict(start=-1), dict(start=2**32), dict(out=out.transpose(1, 3))):
+        a = dict(out=out, codebook=dcb, start=0) | bad
+        with pytest.raises(ValueError):
+            call(cache, a["out"], a["codebook"], start=a["start"])
+    with pytest.raises(TypeError):
+        call(cache, out.double(), dcb)
+    with pytest.raises(nsn.NsnError):
+        call(cache, out[:, :1].expand(1, 131, 1, 128), dcb)     # every token onto one row
