@@ -1278,8 +1278,9 @@ RowSet row_set(int64_t rows) {
 // With one query per sequence the own part has 1 to 8 rows per (b, kv-head), which a 128-row tile
 // wastes; the decode kernel reads such a cache faster, but has a fixed cost (its window is one warp's
 // work).  Measured, 8 kv-heads, 4 queries each, whole call behind an 8k prefix, tiles against decode
-// kernel: 16 x 300 own tokens 49 / 70 us, 16 x 1200 64 / 60, 16 x 2200 74 / 60; 64 x 100 78 / 115,
-// 64 x 300 100 / 83, 64 x 2200 242 / 112.  The lengths are on the device: the capacity decides.
+// kernel: 16 x 300 own tokens 47 / 69 us, 16 x 1200 62 / 59, 16 x 2200 71 / 59; 64 x 128 74 / 118,
+// 64 x 200 86 / 88, 64 x 300 95 / 80, 64 x 2200 233 / 110.  The lengths are on the device: the capacity
+// decides.
 bool own_by_decode(int n_queries, int B, int H, int own_capacity) {
   return n_queries == 1 && (int64_t)B * H * (own_capacity / BLK + 4) > 2800;
 }
