@@ -440,13 +440,14 @@ __device__ __forceinline__ void tile_write(const Raw& r, const uint4 (*cb)[PF_RE
     s1 = n.x;
     s2 = n.y;
   }
-  const float ratio = smax > 0.f ? s1 / smax : 0.f;
-  const __half2 b2 = __float2half2_rn(ratio), a2 = __float2half2_rn(ratio * s2);
+  // rows past the block's tokens come out as zeros: both scales 0, whatever their records hold
+  const bool live = row < nvalid;
+  const float ratio = live && smax > 0.f ? s1 / smax : 0.f;
+  const __half2 b2 = __float2half2_rn(ratio), a2 = __float2half2_rn(live ? ratio * s2 : 0.f);
   __syncwarp();  // the previous tile's mean row has been read
   reinterpret_cast<uint2*>(orow)[lane] = mean;
   __syncwarp();
   unsigned char* dst = tile + row * 128;
-  const bool live = row < nvalid;
   const uint4* rep = &cb[0][lane & (PF_REP - 1)];
   const uint32_t sw[4] = {r.sign.x, r.sign.y, r.sign.z, r.sign.w};
   // Four sub-vectors at a time, the next four's reads before this four's writes: the compiler keeps
@@ -478,8 +479,7 @@ __device__ __forceinline__ void tile_write(const Raw& r, const uint4 (*cb)[PF_RE
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) u[i] = as_u32(__hfma2(as_h2(u[i]), a2, __hmul2(as_h2(om[i]), b2)));
-      *reinterpret_cast<uint4*>(dst + (s >> 3) * PF_HALF + (((s & 7) ^ (row & 7)) << 4)) =
-          live ? make_uint4(u[0], u[1], u[2], u[3]) : make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(dst + (s >> 3) * PF_HALF + (((s & 7) ^ (row & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
     }
   }
 }
