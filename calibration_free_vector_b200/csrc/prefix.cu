@@ -27,7 +27,18 @@
 // they are of order one whatever the norms are; smax of K multiplies the scores, log2 smax of
 // V goes into the exponent (so w is scaled by what it contributes, not by what it weighs) and
 // its inverse into the denominator.  Rounding to fp16 happens at q~, y and w (2^-11 relative
-// at most each); sums, maxima and the denominator are fp32.
+// at most each; y has three: its scale, its mean's product, its sum); sums, maxima and the
+// denominator are fp32.
+//
+// What bounds it.  Per 128 tokens and 256 rows the products take 2048 tensor cycles, the
+// exponentials 2048, the operands and the decoding about 3900 of shared memory.  Measured (2-bit,
+// 8 kv-heads): 256 rows per kv-head over 131072 tokens 168 us, 54 % of the cycles in the tensor
+// cores; 4096 rows over 32768 tokens 565 us, 0.97 PFLOP/s.  A tile takes about 4700 cycles: the
+// decode teams' instructions (one warp of each per scheduler, some 600 a tile) and the softmax share
+// the issue slots.  What brought it there, at 4096 rows: two decode teams, half tiles in flight and an
+// MMA warp per group 745 -> 609 us, codeword reads ahead of writes 609 -> 573.  Not kept: one buffer
+// of half tiles instead of two whole ones, with room for 8 replicas (668), three buffers with one
+// decode team (745), softmax turns between the groups (no change).
 
 #include "hadamard_mma.cuh"
 #include "nsn_launch.h"
@@ -54,7 +65,7 @@ constexpr uint32_t PF_HALF = 16384u;
 constexpr float PF_SLACK = 8.0f;
 #define NEG_INF __int_as_float(0xFF800000)
 constexpr uint32_t PF_WAIT_LIMIT = 1u << 22;   // attempts of a wait before it gives up (seconds)
-constexpr uint32_t PF_POLL_LIMIT = 1u << 26;   // idle rounds of the MMA thread's event loop (seconds)
+constexpr uint32_t PF_POLL_LIMIT = 1u << 26;   // idle rounds of an MMA warp's event loop (seconds)
 
 struct RowSet {  // the rows of one kind of segment
   int rows;      // query rows of a segment
@@ -159,9 +170,10 @@ __device__ __forceinline__ void tc_commit_to(uint64_t* b) {
 constexpr uint32_t PF_IDESC_QK = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t PF_IDESC_PV = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 
-// The K = 16 steps of one product, issued by one elected lane of a converged warp: with operands uniform across the warp the compiler keeps them in uniform registers.  From a
-// single-lane branch, where each operand is moved there first, an MMA took over 100 cycles to issue
-// beside the busy warps, twice its execution.  A descriptor is its low word (start address and leading
+// The K = 16 steps of one product, issued by one elected lane of a converged warp: with operands uniform
+// across the warp the compiler keeps them in uniform registers.  From a single-lane branch, where each
+// operand is moved there first, an MMA took over 100 cycles to issue beside the busy warps, twice its
+// execution.  A descriptor is its low word (start address and leading
 // offset) and the constant high word.
 constexpr uint32_t PF_DESC_HI = (uint32_t)(((1024ull >> 4 << 32) | (1ull << 46) | (2ull << 61)) >> 32);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return ((addr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16); }

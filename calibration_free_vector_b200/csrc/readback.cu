@@ -9,8 +9,13 @@
 // The transform is the one of hadamard_mma.cuh (M = the 16 tokens of a tile).  Its A operand,
 // for each r the 16 values of sub-vectors 2r and 2r + 1, is gathered by ldmatrix straight from an
 // 8-fold replicated fp16 codebook, the stored signs XOR-ed on.  A lane ends with four consecutive
-// dims of a row: 8- or 16-byte stores, every 32-byte sector written whole (rows sent through shared
-// memory with one bulk copy each were no faster: 275 against 266 us for 16 x 8 x 32768 bf16 rows).
+// dims of a row: 8- or 16-byte stores, every 32-byte sector written whole.
+//
+// Bytes bound it: a 2-bit token is 38 bytes read and 256 (bf16) written.  Measured on 16 x 8 x 32768
+// 2-bit tokens to bf16: 266-280 us, 4.4-4.6 TB/s, 67-70 % of the copy bandwidth; DRAM traffic is the
+// 1.18 GB that it has to be.  Warps wait for their reads behind the stores' traffic.  Measured and not
+// kept: rows sent through shared memory by one bulk copy each (275 us) or by stores of two whole rows
+// (259, ragged batches slower), reads two tiles ahead (257, ragged batches slower).
 
 #include "hadamard_mma.cuh"
 #include "nsn_launch.h"
