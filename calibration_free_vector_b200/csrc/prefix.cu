@@ -63,7 +63,6 @@ constexpr uint32_t PF_HALF = 16384u;
 // The running max moves only when a score exceeds it by more than this (log2 units): w stays
 // below 2^8, and most tiles leave O alone.
 constexpr float PF_SLACK = 8.0f;
-#define NEG_INF __int_as_float(0xFF800000)
 constexpr uint32_t PF_WAIT_LIMIT = 1u << 22;   // attempts of a wait before it gives up (seconds)
 constexpr uint32_t PF_POLL_LIMIT = 1u << 26;   // idle rounds of an MMA warp's event loop (seconds)
 
@@ -263,6 +262,7 @@ __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) 
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ float minus_inf() { return __int_as_float(0xFF800000); }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -944,7 +944,7 @@ __device__ __forceinline__ bool softmax_role(const PfArgs& a, PfSmem& sm, Cursor
             mask_scores(sa, limit);
             mask_scores(sb, limit - 32);
           }
-          float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+          float mx[4] = {minus_inf(), minus_inf(), minus_inf(), minus_inf()};
 #pragma unroll
           for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], fmaxf(__uint_as_float(sa[i]), __uint_as_float(sb[i])));
           const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), info.ka, info.lv);

@@ -362,9 +362,11 @@ nsn_status nsn_extend_attention(const nsn_cache* k_cache, const nsn_cache* v_cac
  * Queries, reconstructed rows and softmax weights are rounded to fp16 for the tensor
  * cores (rows relative to the largest norm of their 128-token block); sums are fp32.  An
  * output is off by about 5e-4 of its size, whatever out_dtype is.
+ * A query that sees a value which is not finite yields NaN.
  * Three kernel launches (the queries, the attention, the join), and before them the kernel of
- * nsn_decode_attention for the own caches where these are large (by batch and capacity).  Status bit 2 of k_cache->status is set if a wait inside the kernel
- * ran out (the outputs are then not meaningful).
+ * nsn_decode_attention for the own caches where these are large (by batch and capacity).
+ * Status bit 2 of k_cache->status is set if a wait inside the kernel ran out (the outputs are
+ * then not meaningful).
  */
 size_t nsn_prefix_workspace_bytes(const nsn_cache* prefix_k, const nsn_cache* k_cache, int n_q_heads,
                                   int n_queries);

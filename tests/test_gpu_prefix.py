@@ -346,3 +346,48 @@ def test_prefix_refuses_what_it_cannot_take():
         nsn.nsn_decode_attention_prefix(caches[2], caches[3], *caches[2:], q, SCALE, dk, dv, out, ws)
     with pytest.raises(ValueError):
         nsn.prefix_workspace(caches[0], caches[2], 6)
+
+
+def test_one_workspace_serves_decode_and_chunks_in_turn():
+    # own caches large enough for the decode kernel, whose counters stay at zero through the chunk calls
+    B, H, g, C = 64, 2, 4, 12
+    own = [[(128 * ((b + h) % 4), 12 + (b + 5 * h) % 100) for h in range(H)] for b in range(B)]
+    caches = make([(384, 7), (256, 128)], own, 2, 2, False, seed=91, cap=2304)
+    cbk, cbv, dk, dv = books(2, 2)
+    size = max(nsn.nsn_prefix_workspace_bytes(caches[0], caches[2], H * g, n) for n in (1, C))
+    ws = torch.zeros((size,), dtype=torch.uint8, device="cuda")
+    q1, qc = queries((B, H * g, 128), torch.bfloat16, 19), queries((B, C, H * g, 128), torch.bfloat16, 20)
+    got = []
+    for _ in range(2):
+        o1, oc, oe = torch.empty_like(q1), torch.empty_like(qc), torch.empty_like(q1)
+        nsn.nsn_decode_attention_prefix(*caches, q1, SCALE, dk, dv, o1, ws)
+        nsn.nsn_extend_attention_prefix(*caches, qc, SCALE, dk, dv, oc, ws)
+        nsn.nsn_extend_attention_prefix(*caches, q1[:, None], SCALE, dk, dv, oe[:, None], ws)
+        got.append((o1, oc, oe))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert torch.equal(got[0][0], got[0][2])     # a chunk of one is a decode step
+    pick = {(b, h) for b in (0, 9, 33, 63) for h in range(H)}
+    pt.check(*caches, q1, got[0][0], cbk, cbv, 2, 2, SCALE, pick=pick)
+    pt.check(*caches, qc, got[0][1], cbk, cbv, 2, 2, SCALE, chunk=C, pick=pick)
+
+
+def test_decode_prefix_in_a_graph_with_large_own_caches():
+    # three overlapping launches behind the decode kernel, captured and replayed
+    B, H, g = 64, 2, 4
+    own = [[(128 * ((b + h) % 3), (b + 5 * h) % 100) for h in range(H)] for b in range(B)]
+    caches = make([(640, 7)] * H, own, 2, 1, True, seed=93, cap=2304)
+    cbk, cbv, dk, dv = books(2, 1)
+    q = queries((B, H * g, 128), torch.float16, 21)
+    ws = nsn.prefix_workspace(caches[0], caches[2], H * g)
+    want, out = torch.empty_like(q), torch.empty_like(q)
+    nsn.nsn_decode_attention_prefix(*caches, q, SCALE, dk, dv, want, ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            nsn.nsn_decode_attention_prefix(*caches, q, SCALE, dk, dv, out, ws)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
