@@ -92,12 +92,14 @@ struct PfArgs {
   int32_t* status;
 };
 
-struct PfInfo {            // of one tile, for the softmax
-  float ka, lv, iva;       // K scale, log2 and inverse of the V scale
+struct PfInfo {            // of one K tile, for the softmax
+  float ka;                // scale
   int nvalid;              // tokens
-  int vbad;                // first token whose V row is not finite (128: none)
-  int base;                // window tile of a causal segment: query c sees base + c tokens; else nvalid, step 0
-  int step;
+  int base, step;          // a query at chunk position c sees base + step c of them (window tile of a causal segment)
+};
+struct PfInfoV {           // of one V tile
+  float lv, iva;           // log2 and inverse of its scale
+  int vbad;                // first token whose row is not finite (128: none)
   int pad;
 };
 
@@ -108,9 +110,10 @@ struct PfSmem {
   alignas(128) uint4 cbv[NCODES][PF_REP];
   alignas(16) unsigned char o[PF_DEQ_WARPS][256];  // the mean row of the tile a decode warp is at
   alignas(16) PfInfo info[4];
-  float red[2][2][2][PF_TEAM];     // per team (double-buffered: window tiles in turn): K and V scales
+  alignas(16) PfInfoV info_v[4];
+  float red[2][2][PF_TEAM];        // per team (double-buffered: window tiles in turn): the tile's scale
   int red_bad[2][2][PF_TEAM];
-  alignas(8) uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], full[2][PF_BUFS], empty[2][PF_BUFS], meet[2], drain[2];
+  alignas(8) uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], full[2][PF_BUFS], empty[2][PF_BUFS], meet[2], v_info[4], drain[2];
   long long scan[PF_THREADS / 32];
   long long units;
   int seg0, rt0, u0;
@@ -573,97 +576,88 @@ __device__ __forceinline__ bool decode_sync(PfSmem& sm, int team, uint32_t& phas
 }
 
 // One decode warp's walk over the pieces: the K team (TV = false) or the V team; the next tile's
-// global reads are issued before the current one waits for its slot.  The K team also leaves
-// each tile's scales for the softmax.
+// global reads are issued before the current one waits for its buffer.  Each team leaves its tiles'
+// scales for the softmax: K's with the tile itself, V's, which the softmax needs before the tile, as
+// soon as they are known (a slot's last reader was done before the team could get this far).
 template <int MODE, bool DQ, bool TV>
 __device__ __forceinline__ bool decode_role(const PfArgs& a, PfSmem& sm, Cursor cur, int w, int lane) {
   Piece p;
   int tg0 = 0;        // tiles of the CTA before this piece
   uint32_t met = 0;
   unsigned char* orow = sm.o[w + (TV ? PF_TEAM : 0)];
+  const auto leave_v = [&](int g, float smax, int vbad) {
+    if (w == 0 && lane == 0) {
+      PfInfoV v;
+      v.iva = smax > 0.f ? smax : 1.f;
+      v.lv = log2f(v.iva);
+      v.iva = 1.f / v.iva;
+      v.vbad = vbad;
+      v.pad = 0;
+      sm.info_v[g & 3] = v;
+      bar_arrive(&sm.v_info[g & 3]);
+    }
+  };
   while (next_piece(a, cur, p)) {
-    const CacheView& kc = p.own ? a.k : a.pk;
-    const CacheView& vc = p.own ? a.v : a.pv;
+    const CacheView& c = p.own ? (TV ? a.v : a.k) : (TV ? a.pv : a.pk);
     const int64_t seq = p.own ? p.seg - a.H : p.seg;
-    const Src src = seq_src<DQ>(TV ? vc : kc, seq), vs = seq_src<DQ>(vc, seq);
+    const Src src = seq_src<DQ>(c, seq);
     Raw next, raw;
-    uint4 v4 = make_uint4(0u, 0u, 0u, 0u);   // V norms of a K tile's block (for the tile's scales)
-    uint2 vp = make_uint2(0u, 0u);
     const auto fetch = [&](int t) {
-      const int blk = p.j + t;
-      if (blk >= p.s.blocks) return;
-      raw_load<MODE, DQ>(next, src, blk, w, lane);
-      if constexpr (!TV) four_load<DQ>(v4, vp, vs, blk, lane);
+      if (p.j + t < p.s.blocks) raw_load<MODE, DQ>(next, src, p.j + t, w, lane);
     };
     fetch(0);
     for (int t = 0; t < p.m; ++t) {
       raw = next;
-      const uint4 c4 = v4;
-      const uint2 cp = vp;
       if (t + 1 < p.m) fetch(t + 1);
       const int g = tg0 + t, buf = g & 1, blk = p.j + t;
-      if (g >= PF_BUFS && !bar_wait(&sm.empty[TV][buf], (uint32_t)(g / PF_BUFS - 1), &sm.fail)) return false;
       unsigned char* tile = sm.kv[TV][buf];
       PfInfo info;
+      float smax;
       if (blk < p.s.blocks) {
         const int nvalid = min(BLK, p.s.nq - BLK * blk);
-        const float smax = block_smax<DQ>(raw.four, raw.par, nvalid, lane);
+        smax = block_smax<DQ>(raw.four, raw.par, nvalid, lane);
+        if constexpr (TV) leave_v(g, smax, BLK);
+        if (g >= PF_BUFS && !bar_wait(&sm.empty[TV][buf], (uint32_t)(g / PF_BUFS - 1), &sm.fail)) return false;
         tile_write<MODE, DQ>(raw, TV ? sm.cbv : sm.cbk, tile, orow, smax, nvalid, w, lane);
-        if constexpr (!TV) {
-          const float vmax = block_smax<DQ>(c4, cp, nvalid, lane);
-          info.ka = smax > 0.f ? smax : 1.f;
-          info.iva = vmax > 0.f ? vmax : 1.f;
-          info.vbad = BLK;
-          info.nvalid = info.base = nvalid;
-          info.step = 0;
-        }
+        info.nvalid = info.base = nvalid;
+        info.step = 0;
       } else {
-        // the team's scale over the whole tile; the K team takes V's along
-        float smax = 0.f, vmax = 0.f;
         int vbad = BLK;
         uint32_t f[8][4];
         const uint32_t side = met & 1;
+        smax = 0.f;
 #pragma unroll 1
-        for (int i = 0; i < (TV ? 2 : 4); ++i) {
+        for (int i = 0; i < 2; ++i) {
           float mine;
           int bad;
-          const bool of_v = TV || i < 2;
-          window_load(f, of_v ? vc : kc, seq, p.s.nw, 2 * w + (i & 1), lane);
-          window_scan(f, 2 * w + (i & 1), lane, mine, bad);
-          if (of_v) {
-            vmax = fmaxf(vmax, mine);
-            vbad = min(vbad, bad);
-          } else {
-            smax = fmaxf(smax, mine);
-          }
+          window_load(f, c, seq, p.s.nw, 2 * w + i, lane);
+          window_scan(f, 2 * w + i, lane, mine, bad);
+          smax = fmaxf(smax, mine);
+          vbad = min(vbad, bad);
         }
         if (lane == 0) {
-          sm.red[TV][side][0][w] = smax;
-          sm.red[TV][side][1][w] = vmax;
+          sm.red[TV][side][w] = smax;
           sm.red_bad[TV][side][w] = vbad;
         }
         if (!decode_sync(sm, TV, met, lane)) return false;
 #pragma unroll
         for (int x = 0; x < PF_TEAM; ++x) {
-          smax = fmaxf(smax, sm.red[TV][side][0][x]);
-          vmax = fmaxf(vmax, sm.red[TV][side][1][x]);
+          smax = fmaxf(smax, sm.red[TV][side][x]);
           vbad = min(vbad, sm.red_bad[TV][side][x]);
         }
+        if constexpr (TV) leave_v(g, smax, vbad);
+        if (g >= PF_BUFS && !bar_wait(&sm.empty[TV][buf], (uint32_t)(g / PF_BUFS - 1), &sm.fail)) return false;
 #pragma unroll 1
         for (int i = 1; i >= 0; --i) {  // (the second 16 rows are still in f)
-          if (i == 0) window_load(f, TV ? vc : kc, seq, p.s.nw, 2 * w, lane);
-          window_write(f, TV ? vmax : smax, TV, tile, 2 * w + i, lane);
+          if (i == 0) window_load(f, c, seq, p.s.nw, 2 * w, lane);
+          window_write(f, smax, TV, tile, 2 * w + i, lane);
         }
-        info.ka = smax > 0.f ? smax : 1.f;
-        info.iva = vmax > 0.f ? vmax : 1.f;
-        info.vbad = vbad;
         info.nvalid = p.s.nw;
         info.step = p.own && a.causal ? 1 : 0;
         info.base = info.step ? p.s.nw - a.C + 1 : p.s.nw;
       }
       if (!TV && w == 0 && lane == 0) {
-        info.lv = log2f(info.iva);
-        info.iva = 1.f / info.iva;
+        info.ka = smax > 0.f ? smax : 1.f;
         sm.info[g & 3] = info;
       }
       fence_async();
@@ -931,6 +925,8 @@ __device__ __forceinline__ bool softmax_role(const PfArgs& a, PfSmem& sm, Cursor
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         if (!bar_wait(&sm.s_full[group][h], tiles, &sm.fail)) return false;
+        // (K tile g cannot be there before V tile g - 4 was, so this barrier is never two phases away)
+        if (h == 0 && !bar_wait(&sm.v_info[(tg0 + t) & 3], (uint32_t)((tg0 + t) >> 2), &sm.fail)) return false;
         if (warp_live) {
           tc_after();
           const uint32_t col = s_col + 64u * h;
@@ -938,6 +934,7 @@ __device__ __forceinline__ bool softmax_role(const PfArgs& a, PfSmem& sm, Cursor
           tm_ld32_async(col, sa);
           tm_ld32_async(col + 32u, sb);
           const PfInfo info = sm.info[(tg0 + t) & 3];
+          const PfInfoV iv = sm.info_v[(tg0 + t) & 3];
           const int limit = min(info.nvalid, info.base + info.step * c_of_row) - 64 * h;
           tm_ready64(sa, sb);
           if (__any_sync(0xffffffffu, limit < 64)) {
@@ -947,7 +944,7 @@ __device__ __forceinline__ bool softmax_role(const PfArgs& a, PfSmem& sm, Cursor
           float mx[4] = {minus_inf(), minus_inf(), minus_inf(), minus_inf()};
 #pragma unroll
           for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], fmaxf(__uint_as_float(sa[i]), __uint_as_float(sb[i])));
-          const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), info.ka, info.lv);
+          const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), info.ka, iv.lv);
           // (rows that do not exist hold whatever the operand's memory held: they have no say)
           if (__any_sync(0xffffffffu, row < p.rows && top > m + PF_SLACK)) {
             const float mn = fmaxf(m, top), f = ex2(m - mn);
@@ -959,7 +956,7 @@ __device__ __forceinline__ bool softmax_role(const PfArgs& a, PfSmem& sm, Cursor
               scale_o(o_col, f);
             }
           }
-          const float off = info.lv - m;
+          const float off = iv.lv - m;
           const uint64_t ka2 = pack_f2(info.ka, info.ka), off2 = pack_f2(off, off);
           uint64_t sum[2] = {0ull, 0ull};
           uint32_t w[16];
@@ -969,8 +966,8 @@ __device__ __forceinline__ bool softmax_role(const PfArgs& a, PfSmem& sm, Cursor
           tm_st16(col + 16u, w);
           float a0, a1;
           unpack_f2(add_f2(sum[0], sum[1]), a0, a1);
-          l = fmaf(a0 + a1, info.iva, l);
-          if (limit > info.vbad - 64 * h) l = __int_as_float(0x7fc00000);  // a value it sees is not finite
+          l = fmaf(a0 + a1, iv.iva, l);
+          if (limit > iv.vbad - 64 * h) l = __int_as_float(0x7fc00000);  // a value it sees is not finite
           tm_wait_st();
           tc_before();
         }
@@ -1069,6 +1066,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_kernel(const __grid_cons
       }
     bar_init(&sm.meet[0], PF_TEAM);
     bar_init(&sm.meet[1], PF_TEAM);
+    for (int i = 0; i < 4; ++i) bar_init(&sm.v_info[i], 1);
     bar_init(&sm.drain[0], 1);
     bar_init(&sm.drain[1], 1);
     sm.fail = 0;
