@@ -33,10 +33,11 @@
 // What bounds it.  Per 128 tokens and 256 rows the products take 2048 tensor cycles, the
 // exponentials 2048, the operands and the decoding about 3900 of shared memory.  Measured (2-bit,
 // 8 kv-heads): 256 rows per kv-head over 131072 tokens 168 us, 54 % of the cycles in the tensor
-// cores; 4096 rows over 32768 tokens 565 us, 0.97 PFLOP/s.  A tile takes about 4700 cycles: the
+// cores; 4096 rows over 32768 tokens 572 us, 0.96 PFLOP/s; 64 rows over 32768 tokens 51 us.  A tile takes about 4700 cycles: the
 // decode teams' instructions (one warp of each per scheduler, some 600 a tile) and the softmax share
 // the issue slots.  What brought it there, at 4096 rows: two decode teams, half tiles in flight and an
-// MMA warp per group 745 -> 609 us, codeword reads ahead of writes 609 -> 573.  Not kept: one buffer
+// MMA warp per group 745 -> 609 us, codeword reads ahead of writes 609 -> 573; V's scales left by the V
+// team, at 64 rows 55 -> 51.  Not kept: one buffer
 // of half tiles instead of two whole ones, with room for 8 replicas (668), three buffers with one
 // decode team (745), softmax turns between the groups (no change).
 
@@ -1288,8 +1289,8 @@ RowSet row_set(int64_t rows) {
 // With one query per sequence the own part has 1 to 8 rows per (b, kv-head), which a 128-row tile
 // wastes; the decode kernel reads such a cache faster, but has a fixed cost (its window is one warp's
 // work).  Measured, 8 kv-heads, 4 queries each, whole call behind an 8k prefix, tiles against decode
-// kernel: 16 x 300 own tokens 47 / 69 us, 16 x 1200 62 / 59, 16 x 2200 71 / 59; 64 x 128 74 / 118,
-// 64 x 200 86 / 88, 64 x 300 95 / 80, 64 x 2200 233 / 110.  The lengths are on the device: the capacity
+// kernel: 16 x 300 own tokens 42 / 66 us, 16 x 1200 56 / 55, 16 x 2200 65 / 55; 64 x 128 74 / 113,
+// 64 x 200 83 / 84, 64 x 300 93 / 76, 64 x 2200 213 / 106.  The lengths are on the device: the capacity
 // decides.
 bool own_by_decode(int n_queries, int B, int H, int own_capacity) {
   return n_queries == 1 && (int64_t)B * H * (own_capacity / BLK + 4) > 2800;
