@@ -306,7 +306,7 @@ static nsn_status attention_prefix(const nsn_cache* prefix_k, const nsn_cache* p
                                    const nsn_cache* v_cache, const void* q, int dtype, int n_q_heads, int n_queries,
                                    bool causal, int64_t q_stride_b, int64_t q_stride_t, int64_t q_stride_h,
                                    float softmax_scale, const float* cb_k, const float* cb_v, void* out, int out_dtype,
-                                   void* workspace, size_t ws_bytes, void* stream) {
+                                   void* workspace, size_t ws_bytes, int give_up, void* stream) {
   nsn_status st = check_prefix(prefix_k, k_cache, n_q_heads, n_queries);
   if (st != NSN_OK) return st;
   st = check_prefix(prefix_v, v_cache, n_q_heads, n_queries);
@@ -326,7 +326,7 @@ static nsn_status attention_prefix(const nsn_cache* prefix_k, const nsn_cache* p
     return NSN_ERR_WORKSPACE;
   return cuda_status(nsn::launch_prefix(view(prefix_k), view(prefix_v), view(k_cache), view(v_cache), q, dtype, n_q_heads,
                                         n_queries, causal, q_stride_b, q_stride_t, q_stride_h, softmax_scale, cb_k, cb_v,
-                                        out, out_dtype, workspace, static_cast<cudaStream_t>(stream)));
+                                        out, out_dtype, workspace, give_up, static_cast<cudaStream_t>(stream)));
 }
 
 nsn_status nsn_decode_attention_prefix(const nsn_cache* prefix_k, const nsn_cache* prefix_v, const nsn_cache* k_cache,
@@ -335,7 +335,7 @@ nsn_status nsn_decode_attention_prefix(const nsn_cache* prefix_k, const nsn_cach
                                        const float* cb_v, void* out, int out_dtype, void* workspace, size_t ws_bytes,
                                        void* stream) {
   return attention_prefix(prefix_k, prefix_v, k_cache, v_cache, q, dtype, n_q_heads, 1, false, q_stride_b, 0, q_stride_h,
-                          softmax_scale, cb_k, cb_v, out, out_dtype, workspace, ws_bytes, stream);
+                          softmax_scale, cb_k, cb_v, out, out_dtype, workspace, ws_bytes, -1, stream);
 }
 
 nsn_status nsn_extend_attention_prefix(const nsn_cache* prefix_k, const nsn_cache* prefix_v, const nsn_cache* k_cache,
@@ -344,7 +344,17 @@ nsn_status nsn_extend_attention_prefix(const nsn_cache* prefix_k, const nsn_cach
                                        const float* cb_k, const float* cb_v, void* out, int out_dtype, void* workspace,
                                        size_t ws_bytes, void* stream) {
   return attention_prefix(prefix_k, prefix_v, k_cache, v_cache, q, dtype, n_q_heads, n_queries, true, q_stride_b,
-                          q_stride_t, q_stride_h, softmax_scale, cb_k, cb_v, out, out_dtype, workspace, ws_bytes, stream);
+                          q_stride_t, q_stride_h, softmax_scale, cb_k, cb_v, out, out_dtype, workspace, ws_bytes, -1, stream);
+}
+
+nsn_status nsn_selftest_prefix_give_up(const nsn_cache* prefix_k, const nsn_cache* prefix_v, const nsn_cache* k_cache,
+                                       const nsn_cache* v_cache, const void* q, int dtype, int n_q_heads,
+                                       int64_t q_stride_b, int64_t q_stride_h, float softmax_scale, const float* cb_k,
+                                       const float* cb_v, void* out, int out_dtype, void* workspace, size_t ws_bytes,
+                                       int cta, void* stream) {
+  if (cta < 0) return NSN_ERR_INVALID_ARG;
+  return attention_prefix(prefix_k, prefix_v, k_cache, v_cache, q, dtype, n_q_heads, 1, false, q_stride_b, 0, q_stride_h,
+                          softmax_scale, cb_k, cb_v, out, out_dtype, workspace, ws_bytes, cta, stream);
 }
 
 size_t nsn_decode_rope_workspace_bytes(const nsn_cache* k_cache, int n_q_heads) {

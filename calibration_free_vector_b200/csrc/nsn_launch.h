@@ -73,12 +73,12 @@ cudaError_t launch_extend(const CacheView& kc, const CacheView& vc, const void* 
 
 // Attention over a prefix that the whole batch shares (caches of batch 1) and each
 // sequence's own cache.  `causal`: the last n_queries tokens of every sequence sit in its
-// window and query c sees the window up to its own token.
+// window and query c sees the window up to its own token.  give_up: -1 (see nsn_selftest_prefix_give_up).
 size_t prefix_workspace_bytes(int batch, int n_kv_heads, int g, int n_queries, int own_capacity);
 cudaError_t launch_prefix(const CacheView& pk, const CacheView& pv, const CacheView& k, const CacheView& v, const void* q,
                           int dtype, int n_q_heads, int n_queries, bool causal, int64_t qsb, int64_t qst, int64_t qsh,
                           float softmax_scale, const float* cbk, const float* cbv, void* out, int out_dtype, void* ws,
-                          cudaStream_t s);
+                          int give_up, cudaStream_t s);
 
 // Pre-RoPE keys: the K logits (keys rotated at their positions by inv_freq) into
 // the workspace after the decode partials, then the decode over them.

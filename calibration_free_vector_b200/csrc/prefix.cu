@@ -86,6 +86,8 @@ struct PfArgs {
   RowSet rp, ro;
   unsigned char* qt;       // rotated query tiles: two of hr rows per item, prefix items first
   int2* tab;               // per item: first and last CTA
+  int32_t* bad;            // a CTA gave up: the join writes NaN (and reads neither the table nor partials)
+  int give_up;             // the CTA whose K team gives up at once (-1: none), for the diagnostic of this path
   float2* ml;              // partial (m, l): prefix slots, then own slots
   float* acc;              // partial sums, same slots
   const float* own_out;    // not null: the own part's rows come from the decode kernel (then ro is empty),
@@ -825,6 +827,7 @@ __device__ __forceinline__ unsigned char* q_tile(const PfArgs& a, bool own, int6
 __global__ void __launch_bounds__(32 * QUERY_WARPS) prefix_query_kernel(const __grid_constant__ PfArgs a) {
   const int lane = threadIdx.x & 31, g = lane >> 2, pr = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;");
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.bad = 0;
   const int64_t unit = (int64_t)blockIdx.x * QUERY_WARPS + (threadIdx.x >> 5);
   const int np = (a.rp.rows + 15) / 16, no = (a.ro.rows + 15) / 16;  // 16-row groups of a segment
   const bool own = unit >= (int64_t)a.H * np;
@@ -1010,6 +1013,14 @@ __device__ __forceinline__ bool softmax_role(const PfArgs& a, PfSmem& sm, Cursor
   return true;
 }
 
+// This CTA gave up, so items may lack table entries and partials (by one thread, behind the query kernel, which
+// clears the word).
+__device__ __forceinline__ void report_failure(const PfArgs& a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  *(volatile int32_t*)a.bad = 1;
+  if (a.status) atomicOr(a.status, 2);
+}
+
 template <int MK, int MV, bool DQ>
 __global__ void __launch_bounds__(PF_THREADS, 1) prefix_kernel(const __grid_constant__ PfArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -1017,7 +1028,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_kernel(const __grid_cons
   // (the swizzle needs 1024-byte aligned tiles; there is no room to align by hand, and no static
   // shared memory that could move the base)
   if (sm_addr(smem_raw) & 1023u) {
-    if (threadIdx.x == 0 && a.status) atomicOr(a.status, 2);
+    if (threadIdx.x == 0) report_failure(a);
     return;
   }
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -1080,11 +1091,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_kernel(const __grid_cons
     if (w < warp) before += sm.scan[w];
     total += sm.scan[w];
   }
-  // at least one unit each, so the CTAs with tiles of an item are consecutive
   // The counters and caches were there before the whole call; of the kernels before this one only the
   // query tiles are needed, and whoever copies one waits (griddepcontrol.wait) first.  The join may be
   // scheduled from here on and waits for this kernel's end.
   asm volatile("griddepcontrol.launch_dependents;");
+  // at least one unit each, so the CTAs with tiles of an item are consecutive
   const long long ctas = min((long long)gridDim.x, total), bid = blockIdx.x;
   if (bid >= ctas) {  // the whole CTA: nothing to do (the kernels before this one still end first)
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1127,26 +1138,25 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_kernel(const __grid_cons
     }
   } else if (warp < 16) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PF_REGS_DECODE));
-    ok = warp < 8 + PF_TEAM ? decode_role<MK, DQ, false>(a, sm, cur, warp - 8, lane)
+    ok = warp < 8 + PF_TEAM ? (int)blockIdx.x != a.give_up && decode_role<MK, DQ, false>(a, sm, cur, warp - 8, lane)
                             : decode_role<MV, DQ, true>(a, sm, cur, warp - 8 - PF_TEAM, lane);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PF_REGS_MMA));
     if (warp <= 17) {
       ok = mma_role(a, sm, cur, warp - 16);
-      if (!ok) {  // let MMAs in flight finish before tensor memory is given back
-        int never = 0;
-        tc_commit_to(&sm.drain[warp - 16]);
-        bar_wait(&sm.drain[warp - 16], 0u, &never);
-      }
+      if (!ok) *(volatile int*)&sm.fail = 1;
+      // products in flight finish, and their arrivals land, before tensor memory is given back and the CTA ends
+      // (whichever role gave up)
+      int never = 0;
+      tc_commit_to(&sm.drain[warp - 16]);
+      if (!bar_wait(&sm.drain[warp - 16], 0u, &never)) ok = false;
     }
   }
-  if (!ok) {
-    *(volatile int*)&sm.fail = 1;
-    if (a.status) atomicOr(a.status, 2);
-  }
+  if (!ok) *(volatile int*)&sm.fail = 1;
   __syncwarp();
   tc_before();
   __syncthreads();
+  if (tid == 0 && *(volatile int*)&sm.fail) report_failure(a);
   if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem));
 }
 
@@ -1227,7 +1237,9 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) prefix_join_kernel(const __gr
     tiles_o = a.own_lse ? 0 : seg_info(a, a.H + b * a.H + h).tiles;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (live) {
+  if (*a.bad) {
+    l = __int_as_float(0x7fc00000);
+  } else if (live) {
     if (a.own_lse && wi == 0) {
       own = a.own_lse[r];
       o = *reinterpret_cast<const float4*>(a.own_out + r * D + 4 * lane);
@@ -1316,7 +1328,7 @@ PfLayout layout(int B, int H, int g, int C, int own_capacity) {
   y.own_lse = y.own_out + (dec ? up256((size_t)rows_out * D * sizeof(float)) : 0);
   y.qt = y.own_lse + (dec ? up256((size_t)rows_out * sizeof(float2)) : 0);
   y.tab = y.qt + up256((size_t)(ip * 2 * q_tile_bytes(y.rp) + io * 2 * q_tile_bytes(y.ro)));
-  y.ml = y.tab + up256((size_t)(ip + io) * sizeof(int2));
+  y.ml = y.tab + up256((size_t)(ip + io + 1) * sizeof(int2));  // (and the failure word)
   y.acc = y.ml + up256((size_t)rows * sizeof(float2));
   y.bytes = y.acc + (size_t)rows * D * sizeof(float);
   return y;
@@ -1356,7 +1368,7 @@ size_t prefix_workspace_bytes(int batch, int n_kv_heads, int g, int n_queries, i
 cudaError_t launch_prefix(const CacheView& pk, const CacheView& pv, const CacheView& k, const CacheView& v, const void* q,
                           int dtype, int n_q_heads, int n_queries, bool causal, int64_t qsb, int64_t qst, int64_t qsh,
                           float softmax_scale, const float* cbk, const float* cbv, void* out, int out_dtype, void* ws,
-                          cudaStream_t s) {
+                          int give_up, cudaStream_t s) {
   PfArgs a;
   a.pk = pk; a.pv = pv; a.k = k; a.v = v;
   a.q = q;
@@ -1372,6 +1384,8 @@ cudaError_t launch_prefix(const CacheView& pk, const CacheView& pv, const CacheV
   unsigned char* w = static_cast<unsigned char*>(ws);
   a.qt = w + y.qt;
   a.tab = reinterpret_cast<int2*>(w + y.tab);
+  a.bad = reinterpret_cast<int32_t*>(a.tab + (int64_t)a.H * y.rp.rt + (int64_t)a.B * a.H * y.ro.rt);
+  a.give_up = give_up;
   a.ml = reinterpret_cast<float2*>(w + y.ml);
   a.acc = reinterpret_cast<float*>(w + y.acc);
   a.own_out = nullptr;

@@ -111,6 +111,8 @@ def load():
     lib.nsn_decode_attention_prefix.restype = c_int
     lib.nsn_decode_attention_prefix.argtypes = caches + [c_void_p, c_int, c_int, c_int64, c_int64, c_float, c_void_p,
                                                          c_void_p, c_void_p, c_int, c_void_p, c_size_t, c_void_p]
+    lib.nsn_selftest_prefix_give_up.restype = c_int
+    lib.nsn_selftest_prefix_give_up.argtypes = lib.nsn_decode_attention_prefix.argtypes[:-1] + [c_int, c_void_p]
     lib.nsn_extend_attention_prefix.restype = c_int
     lib.nsn_extend_attention_prefix.argtypes = caches + [c_void_p, c_int, c_int, c_int, c_int64, c_int64, c_int64, c_float,
                                                          c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_size_t, c_void_p]
@@ -438,6 +440,19 @@ def nsn_decode_attention_prefix(prefix_k: Cache, prefix_v: Cache, k_cache: Cache
              ctypes.byref(prefix_k.c), ctypes.byref(prefix_v.c), ctypes.byref(k_cache.c), ctypes.byref(v_cache.c),
              q.data_ptr(), _dtype_code(q), q.shape[1], sb, sh, softmax_scale, cb_k.data_ptr(), cb_v.data_ptr(),
              out.data_ptr(), _dtype_code(out), workspace.data_ptr(), workspace.nbytes)
+
+
+def nsn_selftest_prefix_give_up(prefix_k: Cache, prefix_v: Cache, k_cache: Cache, v_cache: Cache, q, softmax_scale: float,
+                                cb_k, cb_v, out, workspace, cta: int = 0, stream=None) -> None:
+    """nsn_decode_attention_prefix in which CTA `cta` gives up (the error path's diagnostic)."""
+    if q.dim() != 3:
+        raise ValueError("q must be [B, H_q, 128]")
+    device = _check_prefix_call(prefix_k, prefix_v, k_cache, v_cache, q, cb_k, cb_v, out, workspace)
+    sb, sh, _ = q.stride()
+    _call_on(device, stream, load().nsn_selftest_prefix_give_up, "nsn_selftest_prefix_give_up",
+             ctypes.byref(prefix_k.c), ctypes.byref(prefix_v.c), ctypes.byref(k_cache.c), ctypes.byref(v_cache.c),
+             q.data_ptr(), _dtype_code(q), q.shape[1], sb, sh, softmax_scale, cb_k.data_ptr(), cb_v.data_ptr(),
+             out.data_ptr(), _dtype_code(out), workspace.data_ptr(), workspace.nbytes, cta)
 
 
 def nsn_extend_attention_prefix(prefix_k: Cache, prefix_v: Cache, k_cache: Cache, v_cache: Cache, q,

@@ -365,8 +365,8 @@ nsn_status nsn_extend_attention(const nsn_cache* k_cache, const nsn_cache* v_cac
  * A query that sees a value which is not finite yields NaN.
  * Three kernel launches (the queries, the attention, the join), and before them the kernel of
  * nsn_decode_attention for the own caches where these are large (by batch and capacity).
- * Status bit 2 of k_cache->status is set if a wait inside the kernel ran out (the outputs are
- * then not meaningful).
+ * If a wait inside the kernel runs out, the whole call's outputs are NaN and status bit 2 of
+ * k_cache->status is set.
  */
 size_t nsn_prefix_workspace_bytes(const nsn_cache* prefix_k, const nsn_cache* k_cache, int n_q_heads,
                                   int n_queries);
@@ -481,6 +481,19 @@ nsn_status nsn_codebook_4bit_host(float* codebook, int n_values);
  * up, sets bit 2 of *status (device int32) and returns; the context stays usable.
  */
 nsn_status nsn_selftest_bounded_wait(int32_t* status, int max_attempts, void* stream);
+
+/*
+ * Diagnostic of the shared-prefix kernel's error path: nsn_decode_attention_prefix with the
+ * same arguments, in which the warps of CTA `cta` that decode K tiles stop before their first
+ * one, as if a wait had run out.  The rest of that CTA gives up in turn, and the call ends as
+ * documented there: every output NaN, status bit 2; the context, the workspace and the caches
+ * stay usable.  A CTA that has no tile (or does not exist) changes nothing.
+ */
+nsn_status nsn_selftest_prefix_give_up(const nsn_cache* prefix_k, const nsn_cache* prefix_v,
+                                       const nsn_cache* k_cache, const nsn_cache* v_cache, const void* q,
+                                       int dtype, int n_q_heads, int64_t q_stride_b, int64_t q_stride_h,
+                                       float softmax_scale, const float* cb_k, const float* cb_v, void* out,
+                                       int out_dtype, void* workspace, size_t ws_bytes, int cta, void* stream);
 
 /*
  * Diagnostic of the quantizer's tensor-core scores ([TS] Metodologia 3: nearest
