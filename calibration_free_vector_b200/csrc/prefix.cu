@@ -61,9 +61,13 @@ constexpr int PF_BUFS = 2;         // buffers of K tiles, and of V tiles, in sha
 constexpr int PF_REP = 4;          // replicas of each codeword
 constexpr int PF_TILE_BYTES = 32768;  // 128 tokens (or rows) x 128 dims fp16: two 16 KB halves of 64 dims
 constexpr uint32_t PF_HALF = 16384u;
-// The running max moves only when a score exceeds it by more than this (log2 units): w stays
-// below 2^8, and most tiles leave O alone.
-constexpr float PF_SLACK = 8.0f;
+// The reference m_i of a row's weights is set PF_HEAD below its largest score, and moves only when a score
+// exceeds it by more than PF_HEAD + PF_SLACK (log2 units): most tiles leave O alone, and weights stay below 2^15
+// (fp16 ends at 65504).  fp16 steps by 2^-24 at the low end, so a weight is off by at most 2^-32 of the row's
+// largest (or by its rounding), which counts where one token has nearly all the weight and thousands share the
+// rest: with m_i at the largest score, 14k tokens 17.7 nats below a first token lost most of what they weigh
+// (0.2-0.4 % of the output, with its value a twentieth of theirs; now under 0.06 %, the rounding of its row).
+constexpr float PF_HEAD = 7.0f, PF_SLACK = 8.0f;
 constexpr uint32_t PF_WAIT_LIMIT = 1u << 22;   // attempts of a wait before it gives up (seconds)
 constexpr uint32_t PF_POLL_LIMIT = 1u << 26;   // idle rounds of an MMA warp's event loop (seconds)
 
@@ -950,8 +954,8 @@ __device__ __forceinline__ bool softmax_role(const PfArgs& a, PfSmem& sm, Cursor
           for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], fmaxf(__uint_as_float(sa[i]), __uint_as_float(sb[i])));
           const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), info.ka, iv.lv);
           // (rows that do not exist hold whatever the operand's memory held: they have no say)
-          if (__any_sync(0xffffffffu, row < p.rows && top > m + PF_SLACK)) {
-            const float mn = fmaxf(m, top), f = ex2(m - mn);
+          if (__any_sync(0xffffffffu, row < p.rows && top > m + (PF_HEAD + PF_SLACK))) {
+            const float mn = fmaxf(m, top - PF_HEAD), f = ex2(m - mn);
             m = mn;
             l *= f;
             if (t != first || h) {  // O: once the product before this half's has been added

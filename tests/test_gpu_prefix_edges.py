@@ -1,12 +1,39 @@
-"""GPU tests of shared-prefix attention where it could go wrong: a wait that runs out.
-Helpers and the definition are those of test_gpu_prefix and prefix_testlib."""
+"""GPU tests of shared-prefix attention where it could go wrong: a wait that runs out, a token that takes
+nearly all the weight.  Helpers and the definition are those of test_gpu_prefix and prefix_testlib."""
+import numpy as np
 import pytest
 import torch
 
 from calibration_free_vector_b200 import nsn
+import cache_testlib as ct
+import prefix_testlib as pt
 from test_gpu_prefix import SCALE, books, decode, make, own_counts, queries, workspace
 
 pytestmark = pytest.mark.gpu
+
+
+def attend(q, k, v):
+    """One softmax over the rows k / v [n, 128] for queries q [m, 128], in fp64 (numpy): (out, tolerance).
+
+    Tolerance, where few tokens have the weight (prefix_testlib's terms, with hard bounds in place of multiples of
+    a root mean square where one rounding counts alone; rho = 2^-11 / sqrt(3)):
+      - weights: sum p_t |v_t - out| 6 ds_t with ds_t = 2 rho |q~ * y_t| + rho |s_t| + rho, as there, and 2^-32 of
+        the largest weight for each token, where fp16 ends (half a step of 2^-24, weights scaled to 2^7 at least);
+      - rows of V: 2^-11 of each for the scale that its dims share; two roundings per dim, the product with the mean
+        (whose norm is below the row's in these tests) and the sum, which H spreads over the dims: six times
+        sqrt(2) rho sqrt(sum p^2 |v_t|^2 / 128);
+      - fp32 sums and the approximate exponential: 2^-22 of the largest element."""
+    s = q @ k.T * SCALE
+    p = np.exp(s - s.max(1, keepdims=True))
+    top = 1.0 / p.sum(1, keepdims=True)
+    p *= top
+    out = p @ v
+    h = pt.hadamard()
+    ds = 2 * pt.RHO * np.sqrt(((q @ h * SCALE) ** 2) @ ((k @ h) ** 2).T) + pt.RHO * np.abs(s) + pt.RHO
+    tol = np.stack([6 * (pi * di) @ np.abs(v - oi) for pi, di, oi in zip(p, ds, out)])
+    tol += 2.0 ** -32 * top * np.abs(v).sum(0) + 2.0 ** -11 * p @ np.abs(v)
+    tol += 6 * np.sqrt(2.0) * pt.RHO * np.sqrt((p ** 2) @ (v ** 2).sum(1, keepdims=True) / 128)
+    return out, tol + np.abs(out).max(1, keepdims=True) * 2.0 ** -22
 
 
 @pytest.mark.parametrize("B,g,dt,cap", [(4, 4, torch.bfloat16, None), (70, 8, torch.float16, None),
@@ -44,3 +71,25 @@ def test_give_up_refuses_a_negative_cta():
     with pytest.raises(nsn.NsnError):
         nsn.nsn_selftest_prefix_give_up(*caches, q, SCALE, dk, dv, torch.empty_like(q),
                                         workspace(caches[0], caches[2], 4), cta=-1)
+
+
+def test_a_first_token_that_takes_nearly_all_the_weight():
+    # its key scores about 17.7 nats above the other 32767, its value is a twentieth of theirs, and theirs point the
+    # same way.  256 query rows and 64 kv-heads: a partial runs over some 14k tokens.
+    B, H, n, g = 256, 64, 32768, 1
+    caches = make([(n, 0)] * H, [[(0, 0)] * H] * B, 2, 2, False, seed=111, s1_range=(0.2, 0.21), poison=False)
+    pk, pv = caches[:2]
+    pk.norms[:, :, 0, 0] = 1.0
+    pv.norms[..., 0] = 1.0
+    pv.norms[:, :, 0, 0] = 0.05
+    pv.means[:] = pv.means[:, :, :1].clone() * 4
+    cbk, cbv, dk, dv = books(2, 2)
+    k0 = torch.empty((1, 1, H, 128), device="cuda")
+    nsn.nsn_dequantize_kv(pk, k0, dk)
+    lift = torch.linspace(17.5, 17.9, B, device="cuda")[:, None, None]
+    q = k0[0, 0] / (k0[0, 0] ** 2).sum(-1, keepdim=True) * lift / SCALE
+    out = decode(caches, q, dk, dv)
+    for h in (0, 31, 63):
+        want, tol = attend(q[:, h].double().cpu().numpy(), ct.rows(pk, 0, h, cbk, 2), ct.rows(pv, 0, h, cbv, 2))
+        off = np.abs(out[:, h].double().cpu().numpy() - want) / tol
+        assert off.max() <= 1, f"head {h}: {off.max():.3g} tolerances off"
