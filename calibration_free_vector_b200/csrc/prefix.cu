@@ -68,6 +68,10 @@ constexpr uint32_t PF_HALF = 16384u;
 // rest: with m_i at the largest score, 14k tokens 17.7 nats below a first token lost most of what they weigh
 // (0.2-0.4 % of the output, with its value a twentieth of theirs; now under 0.06 %, the rounding of its row).
 constexpr float PF_HEAD = 7.0f, PF_SLACK = 8.0f;
+// The scale of a V tile without a value other than zero (a power of two below every fp16 norm): it adds nothing
+// to the sum, so its scores must not raise the reference of rows that weigh small values; its weights still count
+// in the denominator.
+constexpr float PF_ZERO_V = 9.094947017729282e-13f;  // 2^-40
 constexpr uint32_t PF_WAIT_LIMIT = 1u << 22;   // attempts of a wait before it gives up (seconds)
 constexpr uint32_t PF_POLL_LIMIT = 1u << 26;   // idle rounds of an MMA warp's event loop (seconds)
 
@@ -595,7 +599,7 @@ __device__ __forceinline__ bool decode_role(const PfArgs& a, PfSmem& sm, Cursor 
   const auto leave_v = [&](int g, float smax, int vbad) {
     if (w == 0 && lane == 0) {
       PfInfoV v;
-      v.iva = smax > 0.f ? smax : 1.f;
+      v.iva = smax > 0.f ? smax : PF_ZERO_V;
       v.lv = log2f(v.iva);
       v.iva = 1.f / v.iva;
       v.vbad = vbad;

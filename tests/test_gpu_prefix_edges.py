@@ -1,5 +1,5 @@
 """GPU tests of shared-prefix attention where it could go wrong: a wait that runs out, a token that takes
-nearly all the weight.  Helpers and the definition are those of test_gpu_prefix and prefix_testlib."""
+nearly all the weight, zero values beside small ones.  Helpers and the definition are those of test_gpu_prefix and prefix_testlib."""
 import numpy as np
 import pytest
 import torch
@@ -92,4 +92,29 @@ def test_a_first_token_that_takes_nearly_all_the_weight():
     for h in (0, 31, 63):
         want, tol = attend(q[:, h].double().cpu().numpy(), ct.rows(pk, 0, h, cbk, 2), ct.rows(pv, 0, h, cbv, 2))
         off = np.abs(out[:, h].double().cpu().numpy() - want) / tol
+        assert off.max() <= 1, f"head {h}: {off.max():.3g} tolerances off"
+
+
+@pytest.mark.parametrize("where", ["window", "block"])
+def test_zero_values_beside_small_ones(where):
+    # a token of value zero scores 12 nats above the others, whose values have norms of 1e-5 to 1e-4: it takes part
+    # in the denominator only.  640 kv-heads: most items are whole in one CTA.
+    B, H, g = 3, 640, 2
+    caches = make([(384, 3)] * H, [[(0, 0)] * H] * B, 2, 2, False, seed=121)
+    pk, pv = caches[:2]
+    small = torch.rand(pv.norms.shape[:3], generator=torch.Generator().manual_seed(1)) * 9e-5 + 1e-5
+    pv.norms[..., 0] = small.half().cuda()
+    pv.window_buf.zero_()
+    pv.norms[:, :, :128, 0] = 0
+    cbk, cbv, dk, dv = books(2, 2)
+    k = torch.empty((1, 387, H, 128), device="cuda")
+    nsn.nsn_dequantize_kv(pk, k, dk)
+    k0 = k[0, 385 if where == "window" else 5, :, None]
+    lift = torch.linspace(11.5, 12.5, B * g, device="cuda").view(B, 1, g, 1)
+    q = (k0 / (k0 ** 2).sum(-1, keepdim=True) * lift / SCALE).reshape(B, H * g, 128)
+    out = decode(caches, q, dk, dv)
+    for h in (0, 100, 333, 517, 639):
+        qh, oh = (x[:, h * g:(h + 1) * g].reshape(B * g, 128).double().cpu().numpy() for x in (q, out))
+        want, tol = attend(qh, ct.rows(pk, 0, h, cbk, 2), ct.rows(pv, 0, h, cbv, 2))
+        off = np.abs(oh - want) / tol
         assert off.max() <= 1, f"head {h}: {off.max():.3g} tolerances off"
