@@ -26,7 +26,7 @@
 // Scales: inside a block the fp16 rows are y_t / smax (smax = the largest s1 of the block), so
 // they are of order one whatever the norms are; smax of K multiplies the scores, log2 smax of
 // V goes into the exponent (so w is scaled by what it contributes, not by what it weighs) and
-// its inverse into the denominator.  Rounding to fp16 happens at q~, y and w (2^-11 relative
+// its inverse into the denominator.  (A window tile's scale: window_scale.)  Rounding to fp16 happens at q~, y and w (2^-11 relative
 // at most each; y has three: its scale, its mean's product, its sum); sums, maxima and the
 // denominator are fp32.
 //
@@ -122,7 +122,7 @@ struct PfSmem {
   alignas(16) unsigned char o[PF_DEQ_WARPS][256];  // the mean row of the tile a decode warp is at
   alignas(16) PfInfo info[4];
   alignas(16) PfInfoV info_v[4];
-  float red[2][2][PF_TEAM];        // per team (double-buffered: window tiles in turn): the tile's scale
+  float red[2][2][PF_TEAM], red_base[2][2][PF_TEAM];  // per team (double-buffered: window tiles in turn): the tile's scale
   int red_bad[2][2][PF_TEAM];
   alignas(8) uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], full[2][PF_BUFS], empty[2][PF_BUFS], meet[2], v_info[4], drain[2];
   long long scan[PF_THREADS / 32];
@@ -525,9 +525,10 @@ __device__ __forceinline__ void window_load(uint32_t (&f)[8][4], const CacheView
   }
 }
 
-// The largest root mean square of those rows that are finite, and the first row that is not.
-__device__ __forceinline__ void window_scan(const uint32_t (&f)[8][4], int w, int lane, float& smax, int& bad) {
-  smax = 0.f;
+// The largest mean square of those rows that are finite, that of the rows below `nbase`, and the first row that is
+// not finite.
+__device__ __forceinline__ void window_scan(const uint32_t (&f)[8][4], int w, int lane, int nbase, float& smax, float& sbase, int& bad) {
+  smax = sbase = 0.f;
   bad = BLK;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -539,11 +540,25 @@ __device__ __forceinline__ void window_scan(const uint32_t (&f)[8][4], int w, in
     }
     ss += __shfl_xor_sync(0xffffffffu, ss, 1);
     ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-    if (ss <= 3.0e38f) smax = fmaxf(smax, sqrtf(ss * (1.0f / D)));
-    else bad = min(bad, 16 * w + (lane >> 2) + 8 * i);
+    const int row = 16 * w + (lane >> 2) + 8 * i;
+    if (ss <= 3.0e38f) smax = fmaxf(smax, ss * (1.0f / D));
+    else bad = min(bad, row);
+    if (ss <= 3.0e38f && row < nbase) sbase = fmaxf(sbase, ss * (1.0f / D));
   }
   smax = warp_max(smax);
+  sbase = warp_max(sbase);
   bad = __reduce_min_sync(0xffffffffu, bad);
+}
+
+// The scale of a window tile from those two mean squares: the power of two at or below the root of `sbase`, or 2^-11
+// of the one for `smax` where that is larger (rows are then below 2^12 in the root mean square, elements below
+// 46400; fp16 ends at 65504).  `sbase` is over the rows that every query of a chunk sees, so later tokens of the
+// chunk change no bit of an earlier query unless they are over 2^11 times larger: a power of two scales exactly.
+// From there on the scale follows them, and the other rows keep their precision until they are 2^-12 of it
+// (an element is off by 2^-25 of the scale at most).  0: no row has a value other than zero.
+__device__ __forceinline__ float window_scale(float smax, float sbase) {
+  const int top = ((int)(__float_as_uint(smax) >> 23) - 127) >> 1, base = ((int)(__float_as_uint(sbase) >> 23) - 127) >> 1;
+  return smax > 0.f ? __uint_as_float((uint32_t)(max(top - 11, base) + 127) << 23) : 0.f;
 }
 
 // Four consecutive dims 16 r + 4 p of row t of an operand tile, as fp16 (`half`: bytes between its 64-dim halves).
@@ -636,26 +651,33 @@ __device__ __forceinline__ bool decode_role(const PfArgs& a, PfSmem& sm, Cursor 
         int vbad = BLK;
         uint32_t f[8][4];
         const uint32_t side = met & 1;
+        const bool chunk = p.own && a.causal;
+        const int nbase = chunk ? max(1, p.s.nw - a.C + 1) : p.s.nw;  // rows that every query sees (that sees any)
+        float sbase = 0.f;
         smax = 0.f;
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
-          float mine;
+          float mine, base;
           int bad;
           window_load(f, c, seq, p.s.nw, 2 * w + i, lane);
-          window_scan(f, 2 * w + i, lane, mine, bad);
+          window_scan(f, 2 * w + i, lane, nbase, mine, base, bad);
           smax = fmaxf(smax, mine);
+          sbase = fmaxf(sbase, base);
           vbad = min(vbad, bad);
         }
         if (lane == 0) {
           sm.red[TV][side][w] = smax;
+          sm.red_base[TV][side][w] = sbase;
           sm.red_bad[TV][side][w] = vbad;
         }
         if (!decode_sync(sm, TV, met, lane)) return false;
 #pragma unroll
         for (int x = 0; x < PF_TEAM; ++x) {
           smax = fmaxf(smax, sm.red[TV][side][x]);
+          sbase = fmaxf(sbase, sm.red_base[TV][side][x]);
           vbad = min(vbad, sm.red_bad[TV][side][x]);
         }
+        smax = window_scale(smax, sbase);
         if constexpr (TV) leave_v(g, smax, vbad);
         if (g >= PF_BUFS && !bar_wait(&sm.empty[TV][buf], (uint32_t)(g / PF_BUFS - 1), &sm.fail)) return false;
 #pragma unroll 1
@@ -664,7 +686,7 @@ __device__ __forceinline__ bool decode_role(const PfArgs& a, PfSmem& sm, Cursor 
           window_write(f, smax, TV, tile, 2 * w + i, lane);
         }
         info.nvalid = p.s.nw;
-        info.step = p.own && a.causal ? 1 : 0;
+        info.step = chunk ? 1 : 0;
         info.base = info.step ? p.s.nw - a.C + 1 : p.s.nw;
       }
       if (!TV && w == 0 && lane == 0) {
@@ -957,9 +979,11 @@ __device__ __forceinline__ bool softmax_role(const PfArgs& a, PfSmem& sm, Cursor
 #pragma unroll
           for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], fmaxf(__uint_as_float(sa[i]), __uint_as_float(sb[i])));
           const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), info.ka, iv.lv);
-          // (rows that do not exist hold whatever the operand's memory held: they have no say)
-          if (__any_sync(0xffffffffu, row < p.rows && top > m + (PF_HEAD + PF_SLACK))) {
-            const float mn = fmaxf(m, top - PF_HEAD), f = ex2(m - mn);
+          // (rows that do not exist hold whatever the operand's memory held: they have no say.  A row's own scores
+          // alone move its reference, so its result does not depend on the other rows of the warp)
+          const bool up = row < p.rows && top > m + (PF_HEAD + PF_SLACK);
+          if (__any_sync(0xffffffffu, up)) {
+            const float mn = up ? top - PF_HEAD : m, f = ex2(m - mn);
             m = mn;
             l *= f;
             if (t != first || h) {  // O: once the product before this half's has been added

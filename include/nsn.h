@@ -382,7 +382,10 @@ nsn_status nsn_decode_attention_prefix(const nsn_cache* prefix_k, const nsn_cach
  * (they are its last tokens and all sit in its window), query i of the chunk attends
  *   { prefix tokens } U { own quantized tokens } U { own window slots 0 .. n_window - n_queries + i }
  * with one softmax.  What a later token of the chunk holds does not reach an earlier query
- * (infinities and NaN included).
+ * (infinities and NaN included): the earlier query's output is the same bit for bit, unless a
+ * finite later row's norm is over 2048 times the largest one that every query of the chunk
+ * sees; from there on the window's rows are rounded relative to that row (an element is off
+ * by at most 2^-36 of its root mean square).
  *   q          query (b, i, h) at q + b*q_stride_b + i*q_stride_t + h*q_stride_h, as
  *              nsn_extend_attention; n_queries 1 .. 128, own window 128.
  *   out        device, out_dtype, [batch][n_queries][n_q_heads][128].

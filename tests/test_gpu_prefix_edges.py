@@ -1,5 +1,6 @@
 """GPU tests of shared-prefix attention where it could go wrong: a wait that runs out, a token that takes
-nearly all the weight, zero values beside small ones.  Helpers and the definition are those of test_gpu_prefix and prefix_testlib."""
+nearly all the weight, zero values beside small ones,
+large later tokens of a chunk.  Helpers and the definition are those of test_gpu_prefix and prefix_testlib."""
 import numpy as np
 import pytest
 import torch
@@ -7,7 +8,7 @@ import torch
 from calibration_free_vector_b200 import nsn
 import cache_testlib as ct
 import prefix_testlib as pt
-from test_gpu_prefix import SCALE, books, decode, make, own_counts, queries, workspace
+from test_gpu_prefix import SCALE, books, decode, extend, make, own_counts, queries, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +119,53 @@ def test_zero_values_beside_small_ones(where):
         want, tol = attend(qh, ct.rows(pk, 0, h, cbk, 2), ct.rows(pv, 0, h, cbv, 2))
         off = np.abs(oh - want) / tol
         assert off.max() <= 1, f"head {h}: {off.max():.3g} tolerances off"
+
+
+@pytest.mark.parametrize("B,C,g,own", [(2, 16, 4, [(128, 50), (0, 16)]), (1, 40, 8, [(256, 90)]), (3, 7, 1, [(0, 7), (128, 128), (0, 9)])])
+def test_later_tokens_of_a_chunk_leave_earlier_queries_bit_for_bit(B, C, g, own):
+    # finite rows up to 1500 times the others, infinities and NaN in the last tokens of the chunk: the queries before
+    # them give the same bits (2048 is the documented limit)
+    caches = make([(256, 40)], [[n] for n in own], 2, 2, False, seed=131)
+    _, _, kc, vc = caches
+    _, _, dk, dv = books(2, 2)
+    q = queries((B, C, g, 128), torch.bfloat16, seed=23)
+    clean = extend(caches, q, dk, dv)
+    noise = torch.randn((2, 128), generator=torch.Generator().manual_seed(24)).cuda()
+    for hidden in (1, C // 2):
+        for size in (2e-4, 300.0, 1500.0, float("inf"), float("nan")):
+            saved = [t.window_buf.clone() for t in (kc, vc)]
+            for b, (_, nw) in enumerate(own):
+                kc.window_buf[b, 0, nw - hidden:nw] = (noise[0] * size).half()
+                vc.window_buf[b, 0, nw - hidden:nw] = (noise[1] * size).half()
+            out = extend(caches, q, dk, dv)
+            assert torch.equal(out[:, :C - hidden], clean[:, :C - hidden]), (hidden, size)
+            kc.window_buf.copy_(saved[0])
+            vc.window_buf.copy_(saved[1])
+
+
+def test_a_later_value_400000_times_larger():
+    # past the range in which not a bit changes: keys and values of root mean square 0.05, and a last token (K and V)
+    # of 20000.  Its scale leaves the others 2^-9 of it: an element is off by 2^-25 / 2^-9 = 2^-16 of their root mean
+    # square.  Keys: the score by at most six times |H q scale log2 e| 2^-16 / sqrt(3) 0.05 < 1e-5, and with it the
+    # weights.  Values: 2^-16 each, which H spreads: 6 x 2^-16 / sqrt(3) of a root mean square at most.  Weights: the
+    # reference is 9 (log2) higher, so a weight may differ by the half step 2^-25 where the largest is 2^-2: 2^-23 of
+    # each value.  Normal weights and rows round alike (the scales are powers of two).
+    C, g = 12, 4
+    caches = make([(128, 0)], [[(128, 60)], [(0, 12)]], 2, 2, False, seed=141)
+    _, pv, kc, vc = caches
+    for c in (pv, vc):
+        c.norms[..., 0] = 0.05
+    for c in (kc, vc):
+        c.window_buf.mul_(0.05)
+    cbk, cbv, dk, dv = books(2, 2)
+    q = queries((2, C, g, 128), torch.float32, seed=25)
+    clean = extend(caches, q, dk, dv)
+    for b, nw in enumerate((60, 12)):
+        row = (torch.randn(128, generator=torch.Generator().manual_seed(b)) * 20000).clamp(-60000, 60000).half().cuda()
+        vc.window_buf[b, 0, nw - 1] = kc.window_buf[b, 0, nw - 1] = row
+    out = extend(caches, q, dk, dv)
+    for b, nw in enumerate((60, 12)):
+        v = np.concatenate([ct.rows(pv, 0, 0, cbv, 2), ct.rows(vc, b, 0, cbv, 2)[:-1]])
+        tol = 1e-5 * np.abs(v).max() + 6 * 2.0 ** -16 / np.sqrt(3.0) * 0.05 + 2.0 ** -23 * np.abs(v).sum(0)
+        off = np.abs((out[b, :C - 1] - clean[b, :C - 1]).cpu().numpy()) / tol
+        assert off.max() <= 1, f"sequence {b}: {off.max():.3g} tolerances off"
