@@ -466,10 +466,15 @@ __device__ __forceinline__ void tile_write(const Raw& r, const uint4 (*cb)[PF_RE
     s1 = n.x;
     s2 = n.y;
   }
-  // rows past the block's tokens come out as zeros: both scales 0, whatever their records hold
+  // Rows past the block's tokens come out as zeros: both scales 0, whatever their records hold.  A row that is not
+  // finite comes out as NaN throughout, so that no score with it is minus infinity (0 x infinity is NaN; where smax
+  // is 0, s1 is 0 or NaN).
   const bool live = row < nvalid;
-  const float ratio = live && smax > 0.f ? s1 / smax : 0.f;
-  const __half2 b2 = __float2half2_rn(ratio), a2 = __float2half2_rn(live ? ratio * s2 : 0.f);
+  const __half2 zero2 = __float2half2_rn(0.f);
+  const uint32_t odd = as_u32(__hfma2(as_h2(mean.x), zero2, __hmul2(as_h2(mean.y), zero2))) & 0x7FFF7FFFu;
+  const float bad_mean = __any_sync(0xffffffffu, odd != 0u) ? __int_as_float(0x7fc00000) : 0.f;
+  const float ratio = smax > 0.f ? s1 / smax : s1, scale = ratio * s2;
+  const __half2 b2 = __float2half2_rn(live ? ratio + bad_mean : 0.f), a2 = __float2half2_rn(live ? fmaf(scale, 0.f, scale) : 0.f);
   __syncwarp();  // the previous tile's mean row has been read
   reinterpret_cast<uint2*>(orow)[lane] = mean;
   __syncwarp();
@@ -568,8 +573,8 @@ __device__ __forceinline__ void put4(unsigned char* tile, int64_t half, int t, i
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack_h2(a, b), pack_h2(c, d));
 }
 
-// Writes those rows rotated, fp16(H x / smax); rows that are not finite are zero where `drop`
-// (V: a zero weight would not cancel them).
+// Writes those rows rotated, fp16(H x / smax); rows that are not finite are NaN throughout (no score with
+// them is minus infinity), or zero where `drop` (V: a zero weight would not cancel them).
 __device__ __forceinline__ void window_write(const uint32_t (&f)[8][4], float smax, bool drop, unsigned char* tile, int w, int lane) {
   uint32_t hb[2][2];
   h16_operand(hb, lane);
@@ -586,11 +591,12 @@ __device__ __forceinline__ void window_write(const uint32_t (&f)[8][4], float sm
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     // an element that is not finite reaches every element of its row
-    const bool zero = drop && !(fabsf(E[0][0][2 * i]) <= 3.0e38f);
+    const bool bad = !(fabsf(E[0][0][2 * i]) <= 3.0e38f);
+    const float as = drop ? 0.f : __int_as_float(0x7fc00000);
 #pragma unroll
     for (int r = 0; r < 8; ++r)
-      put4(tile, PF_HALF, 16 * w + (lane >> 2) + 8 * i, r, lane & 3, zero ? 0.f : E[r][0][2 * i] * inv, zero ? 0.f : E[r][0][2 * i + 1] * inv,
-           zero ? 0.f : E[r][1][2 * i] * inv, zero ? 0.f : E[r][1][2 * i + 1] * inv);
+      put4(tile, PF_HALF, 16 * w + (lane >> 2) + 8 * i, r, lane & 3, bad ? as : E[r][0][2 * i] * inv, bad ? as : E[r][0][2 * i + 1] * inv,
+           bad ? as : E[r][1][2 * i] * inv, bad ? as : E[r][1][2 * i + 1] * inv);
   }
 }
 

@@ -1,6 +1,6 @@
 """GPU tests of shared-prefix attention where it could go wrong: a wait that runs out, a token that takes
-nearly all the weight, zero values beside small ones,
-large later tokens of a chunk.  Helpers and the definition are those of test_gpu_prefix and prefix_testlib."""
+nearly all the weight, zero values beside small ones, large later tokens of a chunk, norms that are NaN.
+Helpers and the definition are those of test_gpu_prefix and prefix_testlib."""
 import numpy as np
 import pytest
 import torch
@@ -169,3 +169,23 @@ def test_a_later_value_400000_times_larger():
         tol = 1e-5 * np.abs(v).max() + 6 * 2.0 ** -16 / np.sqrt(3.0) * 0.05 + 2.0 ** -23 * np.abs(v).sum(0)
         off = np.abs((out[b, :C - 1] - clean[b, :C - 1]).cpu().numpy()) / tol
         assert off.max() <= 1, f"sequence {b}: {off.max():.3g} tolerances off"
+
+
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.mark.parametrize("which", ["key", "value"])
+@pytest.mark.parametrize("dq", [False, True])
+def test_a_block_whose_only_norms_are_nan(which, dq):
+    # one token, or a block with zero norms beside it: nothing else sets the block's scale
+    caches = make([(1, 0)], [[(1, 0)], [(128, 0)]], 2, 2, dq, seed=161, prefix_window=0, own_window=0)
+    c = caches[2 if which == "key" else 3]
+    _, _, dk, dv = books(2, 2)
+    q = queries((2, 4, 128), torch.float32, 27)
+    assert torch.isfinite(decode(caches, q, dk, dv)).all()
+    if dq:
+        c.dq_params[:, :, :, :2] = NAN
+    else:
+        c.norms[..., 0] = 0
+        c.norms[:, :, 0, 0] = NAN
+    assert torch.isnan(decode(caches, q, dk, dv)).all()
