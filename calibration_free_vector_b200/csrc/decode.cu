@@ -520,6 +520,10 @@ __device__ __noinline__ void cta_merge(const float* ws, const float* ws_acc, int
   __syncthreads();  // the scratch may be reused by the next merge of this CTA
 }
 
+__device__ __forceinline__ float nan_for_minus_inf(float s) {
+  return s == __int_as_float(0xFF800000) ? __int_as_float(0x7FC00000) : s;
+}
+
 // One warp = one split of one (sequence, head group); GH <= 4 query heads per
 // warp (a group of 8 runs as two head groups).  A split is a contiguous range of
 // 64-token stages (it may start or end inside a 128-token block); the last split
@@ -537,7 +541,9 @@ __device__ __noinline__ void cta_merge(const float* ws, const float* ws_acc, int
 // RP (pre-RoPE keys): the K logits of every quantized and window token come
 // precomputed from rope_scores_kernel (`rscores`, rs_cap tokens per (sequence,
 // head group)); the kernel then reads neither the query nor the K cache.
-template <int GH, int MK, int MV, bool DQ, bool RP = false>
+// LSE: each row's (max, denominator) goes to `lse` for a caller that joins the rows with another
+// part, and a score of minus infinity (a key that is not finite) counts as NaN, as it does there.
+template <int GH, int MK, int MV, bool DQ, bool RP = false, bool LSE = false>
 __global__ void __launch_bounds__(32 * DEC_WARPS, 1)
 decode_kernel(CacheView kc, CacheView vc, const void* __restrict__ q, int dtype, int64_t qsb, int64_t qsh,
               float qscale, const float* __restrict__ cbk_g, const float* __restrict__ cbv_g,
@@ -774,6 +780,7 @@ decode_kernel(CacheView kc, CacheView vc, const void* __restrict__ q, int dtype,
         sc0 = kn.x * fmaf(kn.y, d0, qo0);
         sc1 = kn.x * fmaf(kn.y, d1, qo1);
       }
+      if constexpr (LSE) sc0 = nan_for_minus_inf(sc0), sc1 = nan_for_minus_inf(sc1);
       if (!full && t_stage + tt + t_l >= tok_end) {  // past the end: no weight, and no stale norms
         sc0 = sc1 = NEG_BIG;
         vn = make_float2(0.f, 0.f);
@@ -894,6 +901,7 @@ decode_kernel(CacheView kc, CacheView vc, const void* __restrict__ q, int dtype,
           sc0 = (lo_lane ? S[0] : S[2]) + r0;
           sc1 = (lo_lane ? S[1] : S[3]) + r1;
         }
+        if constexpr (LSE) sc0 = nan_for_minus_inf(sc0), sc1 = nan_for_minus_inf(sc1);
         if (t_l >= rows) sc0 = sc1 = NEG_BIG;  // tokens 8-15 of the tile and rows past the window
         float unused0 = 0.f, unused1 = 0.f;
         lazy_update(sx, sc0, sc1, unused0, unused1);
@@ -951,7 +959,7 @@ decode_kernel(CacheView kc, CacheView vc, const void* __restrict__ q, int dtype,
     const int mb = mseq / kc.n_kv_heads, mhk = mseq % kc.n_kv_heads;
     cta_merge<GH>(ws, ws + acc_offset(P, G), (int64_t)mseq * (nsplit + 1), nsplit, G, mhg * GH,
                   out + (int64_t)mb * out_sb + (int64_t)(mhk * G + mhg * GH) * D,
-                  lse ? lse + (int64_t)mb * n_q_heads + mhk * G + mhg * GH : nullptr, scratch);
+                  LSE ? lse + (int64_t)mb * n_q_heads + mhk * G + mhg * GH : nullptr, scratch);
   }
 }
 
@@ -1354,14 +1362,14 @@ static cudaError_t launch_t(const CacheView& kc, const CacheView& vc, const void
                             int nw_cut, int64_t out_sb, float2* lse) {
   constexpr int GH = G < 4 ? G : 4;  // heads per warp job
   const size_t smem = sizeof(DecSmem);
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<GH, MK, MV, DQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const auto kernel = lse ? decode_kernel<GH, MK, MV, DQ, false, true> : decode_kernel<GH, MK, MV, DQ>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
   const int nwarps = kc.batch * kc.n_kv_heads * geom.nsplit_q * (G / GH);
   dim3 grid((nwarps + DEC_WARPS - 1) / DEC_WARPS);
-  decode_kernel<GH, MK, MV, DQ><<<grid, 32 * DEC_WARPS, smem, s>>>(kc, vc, q, dtype, qsb, qsh, qscale, cbk, cbv,
-                                                               counters, partials, out, n_q_heads, geom, nullptr, 0,
-                                                               nw_cut, out_sb, lse);
+  kernel<<<grid, 32 * DEC_WARPS, smem, s>>>(kc, vc, q, dtype, qsb, qsh, qscale, cbk, cbv, counters, partials, out,
+                                            n_q_heads, geom, nullptr, 0, nw_cut, out_sb, lse);
   return cudaGetLastError();
 }
 

@@ -61,7 +61,8 @@ cudaError_t launch_decode(const CacheView& kc, const CacheView& vc, const void* 
                           int64_t qsb, int64_t qsh, float softmax_scale, const float* cbk, const float* cbv,
                           float* out, void* ws, const DecodeGeom& geom, cudaStream_t s);
 
-// launch_decode that also writes each row's (max in log2 units, denominator) to lse[b][q-head].
+// launch_decode that also writes each row's (max in log2 units, denominator) to lse[b][q-head]; a score of minus
+// infinity (a key that is not finite) makes its row NaN.
 cudaError_t launch_decode_lse(const CacheView& kc, const CacheView& vc, const void* q, int dtype, int n_q_heads,
                               int64_t qsb, int64_t qsh, float softmax_scale, const float* cbk, const float* cbv,
                               float* out, float2* lse, void* ws, const DecodeGeom& geom, cudaStream_t s);

@@ -1314,6 +1314,10 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) prefix_join_kernel(const __gr
   const float ov[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = (v[i] * (PF_INV_SQRT_D * fr) + ov[i] * fo) * inv;
+  // a value that is not finite makes the whole row NaN: own rows of the decode kernel, whose window values keep their
+  // dims, as those of the tiles
+  const float odd = fmaf(v[0], 0.f, fmaf(v[1], 0.f, fmaf(v[2], 0.f, v[3] * 0.f)));  // 0, or NaN
+  if (__any_sync(0xffffffffu, odd != 0.f)) v[0] = v[1] = v[2] = v[3] = __int_as_float(0x7fc00000);
   const int64_t off = r * D + 4 * lane;
   if (odt == NSN_DTYPE_F32) {
     *reinterpret_cast<float4*>(static_cast<float*>(out) + off) = make_float4(v[0], v[1], v[2], v[3]);

@@ -1,5 +1,5 @@
 """GPU tests of shared-prefix attention where it could go wrong: a wait that runs out, a token that takes
-nearly all the weight, zero values beside small ones, large later tokens of a chunk, norms that are NaN.
+nearly all the weight, zero values beside small ones, large later tokens of a chunk, values that are not finite.
 Helpers and the definition are those of test_gpu_prefix and prefix_testlib."""
 import numpy as np
 import pytest
@@ -174,6 +174,47 @@ def test_a_later_value_400000_times_larger():
 INF, NAN = float("inf"), float("nan")
 
 
+@pytest.mark.parametrize("cap", [384, 2304])     # own parts as tiles, and by the decode kernel
+@pytest.mark.parametrize("g,dt", [(1, torch.float32), (2, torch.float16), (4, torch.float32), (8, torch.bfloat16)])
+def test_a_value_that_is_not_finite_gives_nan_whatever_the_capacity(g, dt, cap):
+    # in own windows and own quantized tokens, keys and values: every query that sees one is NaN in all 128 dims, every
+    # other one keeps its bits
+    B, H = 64, 2
+    own = [[(128 * ((b + h) % 3), 3 + (5 * b + h) % 120) for h in range(H)] for b in range(B)]
+    caches = make([(256, 50), (128, 0)], own, 2, 1, False, seed=151, cap=cap)
+    _, _, kc, vc = caches
+    cbk, cbv, dk, dv = books(2, 1)
+    q = queries((B, H * g, 128), dt, 26)
+    clean = decode(caches, q, dk, dv)
+    pt.check(*caches, q, clean, cbk, cbv, 2, 1, SCALE, pick={(b, h) for b in (0, 1, 2, 31, 63) for h in range(H)})
+    # a key's infinity in the dim where the first query is largest, with the sign that makes its score minus infinity
+    hot = q.view(B, H, g, 128)[:, :, 0].abs().argmax(-1)
+    sign = -torch.sign(q.view(B, H, g, 128)[:, :, 0].float().gather(-1, hot[..., None]))[..., 0]
+    bad = {}
+    for i, (t, value) in enumerate([(kc, INF), (kc, NAN), (vc, INF), (vc, -INF), (vc, NAN)]):
+        for j, row in enumerate((0, 2)):      # window rows
+            b, h = 3 * i + j, (i + j) % H
+            dim = int(hot[b, h])
+            t.window_buf[b, h, row, dim] = value * float(sign[b, h]) if t is kc else value
+            bad[b, h] = True
+    for i, (t, name, value) in enumerate([(kc, "s1", INF), (kc, "s2", INF), (kc, "o", INF), (kc, "o", -INF), (kc, "s1", NAN),
+                                          (vc, "s1", INF), (vc, "s2", INF), (vc, "o", INF), (vc, "s2", NAN)]):
+        b, h = [(b, h) for b in range(20, B) for h in range(H) if own[b][h][0] and (b, h) not in bad][5 * i]
+        if name == "o":
+            t.means[b, h, 0, 77] = value
+        else:
+            t.norms[b, h, 100, 0 if name == "s1" else 1] = value
+        bad[b, h] = True
+    out = decode(caches, q, dk, dv)
+    for b in range(B):
+        for h in range(H):
+            got, want = out[b, h * g:(h + 1) * g], clean[b, h * g:(h + 1) * g]
+            if (b, h) in bad:
+                assert torch.isnan(got).all(), (b, h)
+            else:
+                assert torch.equal(got, want), (b, h)
+
+
 @pytest.mark.parametrize("which", ["key", "value"])
 @pytest.mark.parametrize("dq", [False, True])
 def test_a_block_whose_only_norms_are_nan(which, dq):
@@ -189,3 +230,19 @@ def test_a_block_whose_only_norms_are_nan(which, dq):
         c.norms[..., 0] = 0
         c.norms[:, :, 0, 0] = NAN
     assert torch.isnan(decode(caches, q, dk, dv)).all()
+
+
+def test_an_infinity_through_the_quantizer():
+    # as it would get there: a prompt with one infinite key (prefix), another with one infinite value (own cache)
+    B, H, g, T = 2, 2, 4, 300
+    _, _, dk, dv = books(2, 2)
+    x = torch.randn((4, B, T, H, 128), generator=torch.Generator().manual_seed(28)).cuda()
+    x[0, 0, 5, 0, 3] = INF
+    x[3, 1, 200, 1, 9] = -INF
+    pk, pv = nsn.Cache(1, H, 384, 0, 2), nsn.Cache(1, H, 384, 0, 2)
+    kc, vc = nsn.Cache(B, H, 384, 128, 2), nsn.Cache(B, H, 384, 128, 2)
+    for c, rows, book in ((pk, x[0, :1], dk), (pv, x[1, :1], dv), (kc, x[2], dk), (vc, x[3], dv)):
+        nsn.nsn_quantize_kv(c, rows, book)
+    out = decode((pk, pv, kc, vc), queries((B, H * g, 128), torch.float32, 29), dk, dv)
+    nan = torch.isnan(out).view(B, H, g * 128)
+    assert nan.all(-1).tolist() == [[True, False], [True, True]] and nan.any(-1).tolist() == [[True, False], [True, True]]
