@@ -333,8 +333,8 @@ def nsn_dequantize_kv(cache: Cache, out, codebook, start: int = 0, stream=None) 
         raise ValueError("out must be [B, T, H_kv, 128] with a contiguous last dimension")
     if out.shape[0] != cache.batch or out.shape[2] != cache.n_kv_heads:
         raise ValueError("out batch / kv-head count does not match the cache")
-    if not 0 <= start < 2**31:
-        raise ValueError("start must be a token position")
+    if not 0 <= start < 2**31 or out.shape[1] >= 2**31:
+        raise ValueError("start and the number of tokens must be below 2**31")
     _check_codebook(codebook)
     sb, st, sh, _ = out.stride()
     _call_on(_one_device(cache.codes, out, codebook), stream, load().nsn_dequantize_kv, "nsn_dequantize_kv",
