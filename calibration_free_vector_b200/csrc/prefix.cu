@@ -26,16 +26,17 @@
 // Scales: inside a block the fp16 rows are y_t / smax (smax = the largest s1 of the block), so
 // they are of order one whatever the norms are; smax of K multiplies the scores, log2 smax of
 // V goes into the exponent (so w is scaled by what it contributes, not by what it weighs) and
-// its inverse into the denominator.  (A window tile's scale: window_scale.)  Rounding to fp16 happens at q~, y and w (2^-11 relative
-// at most each; y has three: its scale, its mean's product, its sum); sums, maxima and the
-// denominator are fp32.
+// its inverse into the denominator.  (A window tile's scale: window_scale.)  Rounding to fp16
+// happens at q~, y and w (2^-11 relative at most each; y has three: its scale, its mean's product,
+// its sum): the operands of the tensor cores, which in 32 bits would neither fit in shared memory
+// nor reach this rate.  Sums, maxima and the denominator are fp32.
 //
 // What bounds it.  Per 128 tokens and 256 rows the products take 2048 tensor cycles, the
 // exponentials 2048, the operands and the decoding about 3900 of shared memory.  Measured (2-bit,
 // 8 kv-heads): 256 rows per kv-head over 131072 tokens 168 us, 54 % of the cycles in the tensor
-// cores; 4096 rows over 32768 tokens 572 us, 0.96 PFLOP/s; 64 rows over 32768 tokens 51 us.  A tile takes about 4700 cycles: the
-// decode teams' instructions (one warp of each per scheduler, some 600 a tile) and the softmax share
-// the issue slots.  What brought it there, at 4096 rows: two decode teams, half tiles in flight and an
+// cores; 4096 rows over 32768 tokens 572 us, 0.96 PFLOP/s; 64 rows over 32768 tokens 51 us.  A tile
+// takes about 4700 cycles: the decode teams' instructions (one warp of each per scheduler, some 600 a
+// tile) and the softmax share the issue slots.  What brought it there, at 4096 rows: two decode teams, half tiles in flight and an
 // MMA warp per group 745 -> 609 us, codeword reads ahead of writes 609 -> 573; V's scales left by the V
 // team, at 64 rows 55 -> 51.  Not kept: one buffer
 // of half tiles instead of two whole ones, with room for 8 replicas (668), three buffers with one

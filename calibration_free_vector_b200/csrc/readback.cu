@@ -12,7 +12,7 @@
 // dims of a row: 8- or 16-byte stores, every 32-byte sector written whole.
 //
 // Bytes bound it: a 2-bit token is 38 bytes read and 256 (bf16) written.  Measured on 16 x 8 x 32768
-// 2-bit tokens to bf16: 266-280 us, 4.4-4.6 TB/s, 67-70 % of the copy bandwidth; DRAM traffic is the
+// 2-bit tokens to bf16: 279-284 us, 4.3-4.4 TB/s, 66-67 % of the copy bandwidth; DRAM traffic is the
 // 1.18 GB that it has to be.  Warps wait for their reads behind the stores' traffic.  Measured and not
 // kept: rows sent through shared memory by one bulk copy each (275 us) or by stores of two whole rows
 // (259, ragged batches slower), reads two tiles ahead (257, ragged batches slower).

@@ -360,11 +360,19 @@ nsn_status nsn_extend_attention(const nsn_cache* k_cache, const nsn_cache* v_cac
  *                  its counters are left at zero in the same way).  Calls sharing one workspace
  *                  must not overlap on the GPU.
  * Queries, reconstructed rows and softmax weights are rounded to fp16 for the tensor
- * cores (rows relative to the largest norm of their 128-token block); sums are fp32.  An
- * output is off by about 5e-4 of its size, whatever out_dtype is.
- * A query that sees a value which is not finite yields NaN.
+ * cores (rows relative to the largest norm of their 128-token block); sums are fp32.  A score
+ * is then off by about 6e-4 of the root sum of squares of its 128 products and by 3e-4 of
+ * itself, so outputs lose precision with the size of the scores: measured with fp32 out, in
+ * the root mean square and relative to the outputs, 2e-4 for a single token and 1.3e-3 to
+ * 2.5e-3 at scores of a few nats (up to 7e-3 of the row's largest element), where
+ * nsn_decode_attention over a copy of the prefix, which keeps queries and rows exact, is off
+ * by 2e-4.  The rounding to out_dtype comes on top.  Elements of the scaled, rotated query
+ * below 2^-14 and weights below 2^-21 of a row's largest are held to 2^-25 and 2^-32.
+ * A query that sees a value which is not finite yields NaN in all its elements.
  * Three kernel launches (the queries, the attention, the join), and before them the kernel of
- * nsn_decode_attention for the own caches where these are large (by batch and capacity).
+ * nsn_decode_attention for the own caches where these are large (by batch and capacity, not by
+ * the tokens that they hold); the own part then has that kernel's rounding (weights times norms
+ * in fp16: values with norms below about 1e-3 lose precision).
  * If a wait inside the kernel runs out, the whole call's outputs are NaN and status bit 2 of
  * k_cache->status is set.
  */
