@@ -43,15 +43,6 @@ __device__ __forceinline__ float* partial_ml(float* ws, int64_t p, int G, int h)
 // Tensor-core building blocks (mma.sync m16n8k16, fp16 in / fp32 accumulate;
 // ldmatrix gathers of whole 8-dim codewords).
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
 // Two 8x8 matrices (row addresses from lanes 0-15): for A operands whose rows
 // 8-15 repeat rows 0-7, half the shared-memory reads of an x4.
 __device__ __forceinline__ void ldsm_x2(uint32_t addr, uint32_t& r0, uint32_t& r1) {

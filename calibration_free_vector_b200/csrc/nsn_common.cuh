@@ -58,6 +58,15 @@ __device__ __forceinline__ void load8<NSN_DTYPE_F16>(const void* base, int64_t e
   }
 }
 
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// Four 8x8 matrices of 16-bit elements; lane l gives the address of row l & 7 of matrix l >> 3.
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
 // Reads that stay where they are written: the compiler moves ordinary read-only loads down to their
 // use, which would expose their latency once a tile.
 __device__ __forceinline__ uint4 ld_v4(const void* p) {

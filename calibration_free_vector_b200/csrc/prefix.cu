@@ -137,17 +137,16 @@ static_assert(sizeof(PfSmem) <= 232448, "shared memory of one SM");
 // ---------------------------------------------------------------------------
 // Barriers, tensor core and tensor memory
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t sm_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void bar_init(uint64_t* b, uint32_t n) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(sm_addr(b)), "r"(n) : "memory");
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_addr(b)), "r"(n) : "memory");
 }
 __device__ __forceinline__ void bar_arrive(uint64_t* b) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(sm_addr(b)) : "memory");
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_addr(b)) : "memory");
 }
 __device__ __forceinline__ bool bar_test(uint64_t* b, uint32_t parity) {
   uint32_t done;
   asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-               : "=r"(done) : "r"(sm_addr(b)), "r"(parity & 1u) : "memory");
+               : "=r"(done) : "r"(smem_addr(b)), "r"(parity & 1u) : "memory");
   return done != 0;
 }
 // Bounded wait; false if it gave up or another role did.
@@ -156,7 +155,7 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile 
     uint32_t done;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done) : "r"(sm_addr(b)), "r"(parity & 1u) : "memory");
+        : "=r"(done) : "r"(smem_addr(b)), "r"(parity & 1u) : "memory");
     if (done) return true;
     if (*fail) return false;
   }
@@ -173,7 +172,7 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 __device__ __forceinline__ void tc_commit_to(uint64_t* b) {
   asm volatile(
       "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(sm_addr(b)) : "memory");
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(b)) : "memory");
 }
 
 // Matrix descriptors of the 128-byte-swizzled operands (descriptor version 1, layout 2): 8-row
@@ -727,8 +726,8 @@ __device__ __forceinline__ bool mma_role(const PfArgs& a, PfSmem& sm, Cursor cur
   // descriptors differ from these only by constant steps of the start address (16-byte units)
   const uint32_t tmem = (uint32_t)uniform((int)sm.tmem);
   const uint32_t s_col = tmem + 128u * group, o_col = tmem + 256u + 128u * group;
-  const uint32_t q_lo = desc_lo(sm_addr(sm.q[0]), 16u) + TILE * group, k_lo = desc_lo(sm_addr(sm.kv[0][0]), 16u),
-                 v_lo = desc_lo(sm_addr(sm.kv[1][0]), PF_HALF);
+  const uint32_t q_lo = desc_lo(smem_addr(sm.q[0]), 16u) + TILE * group, k_lo = desc_lo(smem_addr(sm.kv[0][0]), 16u),
+                 v_lo = desc_lo(smem_addr(sm.kv[1][0]), PF_HALF);
   uint64_t *s_full = sm.s_full[group], *p_full = sm.p_full[group], *pv_done = sm.pv_done[group];
   Piece p;
   int g0 = 0, pieces = 0;                  // tiles and pieces before this piece
@@ -952,7 +951,7 @@ __device__ __forceinline__ bool softmax_role(const PfArgs& a, PfSmem& sm, Cursor
       const RowSet& r = p.own ? a.ro : a.rp;
       const unsigned char* src = q_tile(a, p.own, p.item, p.dual ? 0 : group);
       const int rows = p.dual ? p.rows : min(128, p.rows - 128 * group);
-      const uint32_t bytes = (uint32_t)((rows + 7) / 8 * 8) * 128u, dst = sm_addr(sm.q[group]), bar = sm_addr(&sm.q_full[group]);
+      const uint32_t bytes = (uint32_t)((rows + 7) / 8 * 8) * 128u, dst = smem_addr(sm.q[group]), bar = smem_addr(&sm.q_full[group]);
       asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(2u * bytes) : "memory");
       bulk_g2s(dst, src, bytes, bar);
       bulk_g2s(dst + PF_HALF, src + (int64_t)r.hr * D, bytes, bar);
@@ -1066,7 +1065,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_kernel(const __grid_cons
   PfSmem& sm = *reinterpret_cast<PfSmem*>(smem_raw);
   // (the swizzle needs 1024-byte aligned tiles; there is no room to align by hand, and no static
   // shared memory that could move the base)
-  if (sm_addr(smem_raw) & 1023u) {
+  if (smem_addr(smem_raw) & 1023u) {
     if (threadIdx.x == 0) report_failure(a);
     return;
   }
@@ -1158,7 +1157,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_kernel(const __grid_cons
     }
   }
   if (warp == 16) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sm_addr(&sm.tmem)));
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   tc_before();

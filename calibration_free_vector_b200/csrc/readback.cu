@@ -32,13 +32,6 @@ struct RbSmem {
   alignas(16) float ho[RB_WARPS][D];  // H o of the unit's block
 };
 
-__device__ __forceinline__ void rb_ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
 __device__ __forceinline__ uint32_t rb_pack(float x, float y, int dt) {
   if (dt == NSN_DTYPE_BF16) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
@@ -107,7 +100,7 @@ readback_kernel(CacheView cv, int start, int n_tokens, const float* __restrict__
     for (int r = 0; r < 8; ++r) sm.cb[tid][(r + tid) & 7] = row;
   }
   __syncthreads();
-  const uint32_t cb_base = (uint32_t)__cvta_generic_to_shared(&sm.cb[0][0]) + (uint32_t)(lane & 7) * 16u;
+  const uint32_t cb_base = smem_addr(&sm.cb[0][0]) + (uint32_t)(lane & 7) * 16u;
 
   uint32_t hb[2][2];
   h16_operand(hb, lane);
@@ -182,7 +175,7 @@ readback_kernel(CacheView cv, int start, int n_tokens, const float* __restrict__
         for (int r = 0; r < 8; ++r) {
           const uint32_t code = __byte_perm(r < 4 ? cur.code.x : cur.code.y, 0u, 0x4440u | (uint32_t)(r & 3));
           uint32_t a[4];
-          rb_ldsm_x4(cb_base + code * 128u, a);
+          ldsm_x4(cb_base + code * 128u, a);
           if constexpr (MODE == NSN_MODE_2BIT) {
             a[0] ^= (cur.sign[0] << (2 * r)) & 0x80008000u;
             a[1] ^= (cur.sign[1] << (2 * r)) & 0x80008000u;
