@@ -246,3 +246,14 @@ def test_an_infinity_through_the_quantizer():
     out = decode((pk, pv, kc, vc), queries((B, H * g, 128), torch.float32, 29), dk, dv)
     nan = torch.isnan(out).view(B, H, g * 128)
     assert nan.all(-1).tolist() == [[True, False], [True, True]] and nan.any(-1).tolist() == [[True, False], [True, True]]
+
+
+def test_broadcast_queries_and_many_row_tiles():
+    # one query row for the whole batch (stride 0), 4800 rows a kv-head; the own parts differ
+    B, H, g = 600, 1, 8
+    caches = make([(640, 77)], [[(128 * (b % 2), b % 129)] for b in range(B)], 1, 2, True, seed=171)
+    cbk, cbv, dk, dv = books(1, 2)
+    q = queries((1, H * g, 128), torch.float16, 30).expand(B, H * g, 128)
+    out = decode(caches, q, dk, dv)
+    assert torch.equal(out, decode(caches, q.contiguous(), dk, dv))
+    pt.check(*caches, q, out, cbk, cbv, 1, 2, SCALE, pick={(b, 0) for b in (0, 1, 31, 32, 33, 299, 598, 599)})
