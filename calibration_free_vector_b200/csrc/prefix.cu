@@ -550,8 +550,8 @@ __device__ __forceinline__ void window_scan(const uint32_t (&f)[8][4], int w, in
     else bad = min(bad, row);
     if (ss <= 3.0e38f && row < nbase) sbase = fmaxf(sbase, ss * (1.0f / D));
   }
-  smax = warp_max(smax);
-  sbase = warp_max(sbase);
+  smax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(smax)));  // (neither is negative)
+  sbase = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sbase)));
   bad = __reduce_min_sync(0xffffffffu, bad);
 }
 

@@ -373,8 +373,9 @@ nsn_status nsn_extend_attention(const nsn_cache* k_cache, const nsn_cache* v_cac
  * nsn_decode_attention for the own caches where these are large (by batch and capacity, not by
  * the tokens that they hold); the own part then has that kernel's rounding (weights times norms
  * in fp16: values with norms below about 1e-3 lose precision).
- * If a wait inside the kernel runs out, the whole call's outputs are NaN and status bit 2 of
- * k_cache->status is set.
+ * If a wait inside the attention kernel runs out, the whole call's outputs are NaN and status
+ * bit 2 of k_cache->status is set; one inside the own caches' decode kernel sets the bit (the
+ * rows that it was at are then not meaningful).
  */
 size_t nsn_prefix_workspace_bytes(const nsn_cache* prefix_k, const nsn_cache* k_cache, int n_q_heads,
                                   int n_queries);
